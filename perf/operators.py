@@ -40,7 +40,7 @@ def listed():
         {"name": "quant, batch", "op": "quant", "n": 8191, "k": 11008, "type": "fp16"},
         # decoding one sequence; decoding a ragged batch with the widest weight; a training step's product
         {"name": "gemm, one token", "op": "gemm", "m": 4096, "k": 4096, "n": 1, "out": "bf16"},
-        {"name": "gemm, 37 tokens", "op": "gemm", "m": 11008, "k": 4096, "n": 37, "out": "fp32"},
+        {"name": "gemm, 37 tokens", "op": "gemm", "m": 11008, "k": 4096, "n": 37, "out": "fp16"},
         {"name": "gemm, batch", "op": "gemm", "m": 28672, "k": 8192, "n": 8192, "out": "bf16"},
         # a small layer with many tokens: few outputs, a long sum; a projection with its pattern kept
         {"name": "wgrad, small layer", "op": "wgrad", "m": 768, "k": 768, "n": 6304, "out": "fp32", "masked": False},
@@ -71,7 +71,7 @@ def draw(rng):
         # up to the listed weights; single tokens, small batches and whole prompts alike
         m, k = _log(rng, 512, 28672), _k(rng, 512, 8192)
         n = rng.choice([_log(rng, 1, 16), _log(rng, 17, 300), _log(rng, 300, 6304)])
-        return {"op": op, "m": m, "k": k, "n": n, "out": rng.choice(["bf16", "fp32"])}
+        return {"op": op, "m": m, "k": k, "n": n, "out": rng.choice(["bf16", "fp16"])}
     m, k = _log(rng, 512, 11008) // 8 * 8, _k(rng, 512, 8192)
     return {"op": op, "m": m, "k": k, "n": _log(rng, 1, 6304), "out": rng.choice(["bf16", "fp32"]),
             "masked": rng.random() < 0.5}
