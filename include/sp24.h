@@ -85,7 +85,8 @@ typedef enum {
     SP24_ERR_HIP = -7     /* the HIP runtime reported an error at launch */
 } sp24_status;
 
-typedef enum { SP24_BF16 = 0, SP24_FP16 = 1, SP24_FP32 = 2, SP24_I8 = 3, SP24_I32 = 4 } sp24_dtype;
+typedef enum { SP24_BF16 = 0, SP24_FP16 = 1, SP24_FP32 = 2, SP24_I8 = 3, SP24_I32 = 4,
+               SP24_FP8 = 5 /* OCP e4m3, the operators of sp24_fp8.h */ } sp24_dtype;
 
 typedef enum { SP24_SCORE_MAGNITUDE = 0, SP24_SCORE_WANDA = 1 } sp24_score;
 
@@ -107,7 +108,7 @@ typedef enum { SP24_ACT_NONE = 0, SP24_ACT_GELU = 1 } sp24_activation;
 int sp24_col_norms(const void* X, int64_t K, int64_t N, int64_t ldx, float* norms, void* stream);
 
 /* Sizes in bytes of the compressed values and metadata of an M x K weight whose kept values have
- * dtype val_dtype (BF16, FP16, FP32 or I8). Host-only, no HIP call. */
+ * dtype val_dtype (BF16, FP16, FP32, I8 or FP8). Host-only, no HIP call. */
 int sp24_compressed_bytes(int64_t M, int64_t K, int val_dtype, int64_t* values_bytes, int64_t* meta_bytes);
 
 /* 2:4 prune and compress (Orin NN design, Chapter 7, section 2.1, Steps 1-2).

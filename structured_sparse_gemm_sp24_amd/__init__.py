@@ -1,6 +1,7 @@
 """sp24: 2:4 structured-sparse prune/compress and sparse GEMM for AMD MI355X (gfx950).
 
-Thin Python binding over the C ABI of ``libsp24.so`` (declared in include/sp24.h): the functions
+Thin Python binding over the C ABI of ``libsp24.so`` (declared in include/sp24.h, and include/sp24_fp8.h for
+the 8-bit floating-point operators, whose functions live in fp8.py and are exported here): the functions
 below have the C entry points' names and only marshal arguments -- torch tensors supply device
 memory and the current HIP stream; every step runs in the library's HIP kernels. If the library is
 not built, or the device is not gfx950, the calls raise; there is no CPU fallback.
@@ -17,22 +18,25 @@ LIB_PATH = os.path.join(_PKG, "libsp24.so")
 
 SP24_OK, SP24_ERR_NULL, SP24_ERR_SHAPE, SP24_ERR_ALIGN = 0, -1, -2, -3
 SP24_ERR_DTYPE, SP24_ERR_ARG, SP24_ERR_DEVICE, SP24_ERR_HIP = -4, -5, -6, -7
-SP24_BF16, SP24_FP16, SP24_FP32, SP24_I8, SP24_I32 = 0, 1, 2, 3, 4
+SP24_BF16, SP24_FP16, SP24_FP32, SP24_I8, SP24_I32, SP24_FP8 = 0, 1, 2, 3, 4, 5
 SP24_SCORE_MAGNITUDE, SP24_SCORE_WANDA = 0, 1
 SP24_FEATURE_MAJOR, SP24_TOKEN_MAJOR = 0, 1
 SP24_ACT_NONE, SP24_ACT_GELU = 0, 1
 
-# every symbol include/sp24.h declares
+# every symbol the headers in include/ declare
 EXPORTS = ("sp24_col_norms", "sp24_compressed_bytes", "sp24_prune_compress", "sp24_prune_mask",
            "sp24_channel_permutation", "sp24_decompress",
            "sp24_gemm_bf16",
            "sp24_gemm_i8", "sp24_gemm_bf16_ex", "sp24_gemm_i8_ex", "sp24_gemm_i8_fused", "sp24_probe_sclk",
            "sp24_bench_dense_tiled_bytes", "sp24_bench_dense_tile", "sp24_bench_gemm_dense_bf16",
            "sp24_bench_stream_read_blocks", "sp24_bench_stream_read",
+           "sp24_quant_fp8", "sp24_rmsnorm_fp8", "sp24_rmsnorm_backward_bytes", "sp24_rmsnorm_backward",
+           "sp24_prune_compress_fp8", "sp24_decompress_fp8", "sp24_gemm_fp8",
+           "sp24_grad_weight_fp8_bytes", "sp24_grad_weight_fp8",
            "sp24_status_string")
 
 _TORCH_TO_SP24 = {torch.bfloat16: SP24_BF16, torch.float16: SP24_FP16, torch.float32: SP24_FP32,
-                  torch.int8: SP24_I8, torch.int32: SP24_I32}
+                  torch.int8: SP24_I8, torch.int32: SP24_I32, torch.float8_e4m3fn: SP24_FP8}
 _SP24_TO_TORCH = {v: k for k, v in _TORCH_TO_SP24.items()}
 
 
@@ -73,6 +77,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sp24_bench_gemm_dense_bf16.argtypes = [P, I64, I64, P, I64, I64, P, I, I64, P]
     lib.sp24_bench_stream_read_blocks.argtypes = [I64, ctypes.POINTER(I64)]
     lib.sp24_bench_stream_read.argtypes = [P, I64, P, P]
+    fp8.bind(lib)
     for fn in EXPORTS[:-1]:
         getattr(lib, fn).restype = I
     lib.sp24_status_string.argtypes = [I]
@@ -123,7 +128,7 @@ def sp24_col_norms(X: torch.Tensor, norms: torch.Tensor | None = None) -> torch.
     return norms
 
 
-_ESIZE = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4, torch.int8: 1}
+_ESIZE = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4, torch.int8: 1, torch.float8_e4m3fn: 1}
 
 
 def sp24_compressed_bytes(M: int, K: int, val_dtype: torch.dtype):
@@ -392,3 +397,8 @@ def sp24_bench_stream_read(src: torch.Tensor, nbytes: int | None = None, sink: t
         raise ValueError("sink too small")
     _check("sp24_bench_stream_read", lib.sp24_bench_stream_read(_ptr(src), nb, _ptr(sink), _stream(src)))
     return sink
+
+
+from . import fp8  # noqa: E402  (needs the names above)
+from .fp8 import (sp24_decompress_fp8, sp24_gemm_fp8, sp24_grad_weight_fp8, sp24_prune_compress_fp8,  # noqa: E402,F401
+                  sp24_quant_fp8, sp24_rmsnorm_backward, sp24_rmsnorm_fp8)

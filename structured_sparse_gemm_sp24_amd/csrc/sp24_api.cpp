@@ -11,31 +11,11 @@
 
 #include "sp24_launch.h"
 
-namespace {
+namespace sp24 {
 
 constexpr int kMaxDevices = 64;
 // 0 = unknown, 1 = gfx950, -1 = other
-std::atomic<int> g_dev_ok[kMaxDevices];
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-int elem_size(int dt) {
-    switch (dt) {
-    case SP24_BF16: case SP24_FP16: return 2;
-    case SP24_FP32: case SP24_I32: return 4;
-    case SP24_I8: return 1;
-    }
-    return 0;
-}
-
-int check_k(int64_t K) { return (K >= 16 && K % 16 == 0) ? SP24_OK : SP24_ERR_SHAPE; }
-
-// Padded dimensions of the compressed form: rows to 16, columns to 128 / value size.
-int64_t padded_m(int64_t M) { return (M + 15) / 16 * 16; }
-int64_t padded_k(int64_t K, int vsz) {
-    const int64_t kt = 128 / vsz;
-    return (K + kt - 1) / kt * kt;
-}
+static std::atomic<int> g_dev_ok[kMaxDevices];
 
 // The current device must be gfx950. Cached per device; the first call asks the runtime.
 int check_device() {
@@ -56,6 +36,32 @@ int check_device() {
     const bool ok = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
     if (dev < kMaxDevices) g_dev_ok[dev].store(ok ? 1 : -1, std::memory_order_relaxed);
     return ok ? SP24_OK : SP24_ERR_DEVICE;
+}
+
+}  // namespace sp24
+
+namespace {
+
+using sp24::check_device;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int elem_size(int dt) {
+    switch (dt) {
+    case SP24_BF16: case SP24_FP16: return 2;
+    case SP24_FP32: case SP24_I32: return 4;
+    case SP24_I8: case SP24_FP8: return 1;
+    }
+    return 0;
+}
+
+int check_k(int64_t K) { return (K >= 16 && K % 16 == 0) ? SP24_OK : SP24_ERR_SHAPE; }
+
+// Padded dimensions of the compressed form: rows to 16, columns to 128 / value size.
+int64_t padded_m(int64_t M) { return (M + 15) / 16 * 16; }
+int64_t padded_k(int64_t K, int vsz) {
+    const int64_t kt = 128 / vsz;
+    return (K + kt - 1) / kt * kt;
 }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? SP24_OK : SP24_ERR_HIP; }
@@ -90,7 +96,8 @@ const char* sp24_status_string(int status) {
 
 int sp24_compressed_bytes(int64_t M, int64_t K, int val_dtype, int64_t* values_bytes, int64_t* meta_bytes) {
     if (!values_bytes || !meta_bytes) return SP24_ERR_NULL;
-    if (val_dtype != SP24_BF16 && val_dtype != SP24_FP16 && val_dtype != SP24_FP32 && val_dtype != SP24_I8)
+    if (val_dtype != SP24_BF16 && val_dtype != SP24_FP16 && val_dtype != SP24_FP32 && val_dtype != SP24_I8 &&
+        val_dtype != SP24_FP8)
         return SP24_ERR_DTYPE;
     if (M < 1) return SP24_ERR_SHAPE;
     int st = check_k(K);

@@ -81,4 +81,45 @@ hipError_t launch_gemm_i8_fewtok(const GemmArgs& g, hipStream_t s);
 bool gemm_i8_tiled_ok(const GemmArgs& g);
 hipError_t launch_gemm_i8_tiled(const GemmArgs& g, hipStream_t s);
 
+// SP24_OK if the current device is gfx950, else SP24_ERR_DEVICE (sp24_api.cpp; cached per device).
+int check_device();
+
+// 8-bit floating point (include/sp24_fp8.h). dtype: 0 BF16, 1 FP16, 2 FP32 (the sp24_dtype numbers).
+hipError_t launch_quant_fp8(const void* X, int dtype, int64_t N, int64_t K, int64_t ldx, uint8_t* codes, int64_t ldc,
+                            uint8_t* scales, int64_t lds, hipStream_t s);
+hipError_t launch_rmsnorm(const void* X, int dtype, int64_t N, int64_t K, int64_t ldx, const void* R, int64_t ldr,
+                          const void* gamma, float eps, void* H, int64_t ldh, uint8_t* codes, int64_t ldc,
+                          uint8_t* scales, int64_t lds, float* rstd, hipStream_t s);
+// Rows of K partial sums that the norm's gradient writes to its workspace.
+int rmsnorm_back_parts(int64_t N, int64_t K);
+hipError_t launch_rmsnorm_back(const void* dY, int dtype, int64_t N, int64_t K, int64_t lddy, const void* H, int64_t ldh,
+                               const float* rstd, const void* gamma, const void* dH, int64_t lddh, void* dX,
+                               int64_t lddx, float* dgamma, void* workspace, hipStream_t s);
+hipError_t launch_prune_compress_fp8(const void* W, int dtype, int64_t M, int64_t K, int64_t ldw, int score,
+                                     const float* norms, uint8_t* values, uint8_t* meta, uint8_t* w_scales,
+                                     hipStream_t s);
+hipError_t launch_decompress_fp8(const uint8_t* values, const uint8_t* meta, const uint8_t* w_scales, int64_t M,
+                                 int64_t K, void* W, bool f32, int64_t ldw, hipStream_t s);
+
+// Token-major product with block scales: X N x K codes, Y N x M.
+struct Fp8GemmArgs {
+    const uint8_t *values, *meta, *ws, *X, *xs;
+    void* Y;
+    int64_t M, K, N, ldx, lds, ldy;
+    bool out_fp16;  // else bf16
+};
+hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s);
+
+// Weight gradient: dY N x M bf16, X N x K codes, dW M x K; meta NULL or the 2:4 pattern of dW.
+struct Fp8GradArgs {
+    const void* dY;
+    const uint8_t *X, *xs, *meta;
+    void *dW, *workspace;
+    int64_t N, M, K, lddy, ldx, lds, ldw;
+    bool out_fp32;
+};
+// Parts that the tokens are split into; with more than one the workspace holds an M x K fp32 matrix for each.
+int grad_weight_parts(int64_t M, int64_t K, int64_t N);
+hipError_t launch_grad_weight(const Fp8GradArgs& g, hipStream_t s);
+
 }  // namespace sp24
