@@ -159,6 +159,7 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s) {
+    if (g.N > 64) return launch_gemm_fp8_tiled(g, s);
     if (g.N <= 16) return launch<1, 1, 2, 8>(g, s);
     if (g.N <= 32) return launch<2, 2, 2, 8>(g, s);
     return launch<4, 2, 2, 4>(g, s);

@@ -109,6 +109,7 @@ struct Fp8GemmArgs {
     bool out_fp16;  // else bf16
 };
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s);
 
 // Weight gradient: dY N x M bf16, X N x K codes, dW M x K; meta NULL or the 2:4 pattern of dW.
 struct Fp8GradArgs {
