@@ -75,8 +75,8 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 __device__ __forceinline__ float code_factor(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 // 2^(s - 127), NaN for 255.
 __device__ __forceinline__ float scale_value(uint32_t s) {
-    const uint32_t b = s == 0 ? 0x00400000u : s << 23;
-    return __uint_as_float(s == 255u ? 0x7FC00000u : b);
+    const uint32_t b = s << 23;
+    return __uint_as_float((b > 0x00400000u ? b : 0x00400000u) + (((s + 1) >> 8) << 22));
 }
 
 // Two fp32 values rounded once (to nearest even) to packed bf16 or fp16.

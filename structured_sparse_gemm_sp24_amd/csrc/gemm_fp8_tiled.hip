@@ -9,9 +9,13 @@
 //   B (codes of X): 128 token rows of 128 bytes; a lane's operand is the two 16-byte units q and q + 4 of its token's
 //     row, and unit u of row n is stored at u ^ ((n >> 1) & 7) ^ 4 (n & 1), which keeps the reads free of bank
 //     conflicts and each 4 lanes of a load on one 64-byte run.
-// A fragment's product of a stage starts from zero, and acc = fma(product, 2^(x scale + w scale), acc): the sums
-// over blocks are fp32 sums of exactly scaled terms. The power of two depends on the lane's token and the wave's 128
-// rows, so it is formed once for a column of eight fragments.
+// The scales ride on the accumulators (Horner's rule). With e_b the exponent of block b's two scales, which depends on
+// the lane's token and the wave's 128 rows, an accumulator holds the sum so far in units of 2^e_b: before block b's
+// matrix instruction adds its products it is multiplied by 2^(e_(b-1) - e_b), exactly, and the last unit is put back
+// in the epilogue. That is four multiplications a fragment and stage; a product from zero and four fused multiply-adds
+// into a second accumulator are six instructions and four registers more, and measured 466 us against ... on
+// 8192^3. A block whose unit is 2^-64 or less of the largest before it in its sum is left out (its token's codes
+// read as zeros), so that no accumulator can overflow: what it would add is below 2^-40 of that largest unit.
 //
 // Loads are buffer loads with LDS destination whose whole byte offset is in the range-checked VGPR operand: rows past
 // M and N, 16-byte units past K (inside a row what follows may be NaN codes, which zero weights would not cancel) and
@@ -25,14 +29,22 @@
 namespace sp24 {
 namespace {
 
-constexpr int BM = 256, BN = 128, BK = 128, WM = 128, WN = 64, FM = WM / 16, FN = WN / 16;
-constexpr int A_BYTES = BM * 64, META_BYTES = BM * 16, B_BYTES = BN * BK;
-constexpr int STAGE_BYTES = A_BYTES + META_BYTES + B_BYTES;
+constexpr int BM = 256, BK = 128, WM = 128, WN = 64, FM = WM / 16, FN = WN / 16;
+constexpr int A_BYTES = BM * 64, META_BYTES = BM * 16;
 constexpr int NBUF = 2;
+constexpr int CHUNK = 8;  // stages whose scales are fetched together
+
+// Tile width: 128 with four waves and two workgroups a compute unit, or 256 with eight waves.
+template <int BN_>
+struct Cfg {
+    static constexpr int BN = BN_, WAVES = BN_ / 32;
+    static constexpr int STAGE_BYTES = A_BYTES + META_BYTES + BN * BK;
+    static constexpr int CHUNK_BYTES = BN * CHUNK * 4;  // a word for each scale
+    static constexpr int LDS_BYTES = NBUF * STAGE_BYTES + 2 * CHUNK_BYTES;
+    static_assert((BN == 128 ? 2 : 1) * LDS_BYTES <= 160 * 1024, "the workgroups of a compute unit fit in its LDS");
+};
 constexpr int GROUP_M = 8;
 constexpr uint32_t OOR = 0x80000000u;  // a byte offset past every record count
-static_assert(2 * NBUF * STAGE_BYTES <= 160 * 1024, "two workgroups' stage buffers fit in LDS");
-
 struct Args {
     const uint8_t *values, *meta, *ws, *X, *xs;
     void* Y;
@@ -58,6 +70,11 @@ __device__ __forceinline__ void dma16(uint32_t lds, uint32_t voff, const i32x4& 
     asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc) : "memory");
 }
 
+// One byte a lane, zero-extended to the word at lds + 4 i.
+__device__ __forceinline__ void dma1(uint32_t lds, uint32_t voff, const i32x4& rsrc) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(rsrc) : "memory");
+}
+
 __device__ __forceinline__ void wait_vmcnt0() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
@@ -68,6 +85,7 @@ struct Tile {
 
 // Logical tile of workgroup p at its k-th turn (see the int8 kernel's numbering: turn k covers tiles [kG, kG + rem),
 // split evenly over the 8 XCDs, workgroup p on XCD p % 8), walked in groups of GROUP_M tile-rows.
+template <int BN>
 __device__ __forceinline__ Tile tile_of(const Args& a, int p, int k) {
     const int G = gridDim.x, T = a.tilesM * a.tilesN;
     const int64_t base = (int64_t)k * G;
@@ -96,10 +114,11 @@ struct Desc {
     int wrow;          // byte offset of the wave's row of weight scales
 };
 
+template <int BN>
 __device__ __forceinline__ Desc desc_of(const Args& a, const Tile& t, int wave, int wm0) {
     Desc d;
     const int64_t left = (a.M + 15) / 16 - t.m0 / 16, blocks = left < BM / 16 ? left : BM / 16;
-    const int64_t tiles = a.S, n1 = t.n0 + (BN / 4) * wave;
+    const int64_t tiles = a.S, n1 = t.n0 + 32 * wave;
     d.rA = make_rsrc(a.values + (t.m0 / 16) * tiles * 1024, t.valid ? blocks * tiles * 1024 : 0);
     d.rM = make_rsrc(a.meta + (t.m0 / 16) * tiles * 256, t.valid ? blocks * tiles * 256 : 0);
     const int64_t sb = (a.N - 1 - t.n0) * a.lds + a.S;
@@ -113,7 +132,8 @@ __device__ __forceinline__ Desc desc_of(const Args& a, const Tile& t, int wave, 
 
 __device__ __forceinline__ int swz(int n) { return ((n >> 1) & 7) ^ ((n & 1) << 2); }
 
-// This wave's share of the loads of stage s: values of row blocks 4 wave .. +3, their metadata, 32 token rows.
+// A wave's share of the loads of a stage: values of 16 / WAVES row blocks, the metadata of four (waves 0 .. 3), 32
+// token rows.
 struct LoadOffsets {
     uint32_t a, m, b[4];
     int unit[2];  // dense column of the 16-byte unit that load h (parity h & 1) takes
@@ -132,13 +152,15 @@ __device__ __forceinline__ LoadOffsets load_offsets(const Args& a, int lane) {
     return o;
 }
 
+template <int BN>
 __device__ __forceinline__ void load_stage(uint32_t lds, const Args& a, const Desc& d, int s, int wave, const LoadOffsets& lo) {
+    constexpr int AL = 16 / Cfg<BN>::WAVES;
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const int b = 4 * wave + j;
+    for (int j = 0; j < AL; j++) {
+        const int b = AL * wave + j;
         dma16(lds + b * 1024, lo.a + (uint32_t)(b * a.S + s) * 1024u, d.rA);
     }
-    dma16(lds + A_BYTES + 4 * wave * 256, lo.m + (uint32_t)(4 * wave * a.S + s) * 256u, d.rM);
+    if (AL == 4 || wave < 4) dma16(lds + A_BYTES + 4 * wave * 256, lo.m + (uint32_t)(4 * wave * a.S + s) * 256u, d.rM);
     const int k0 = s * BK, left = (int)a.K - k0;
     const i32x4 rB = make_rsrc(d.x + k0, d.xbytes - k0);
 #pragma unroll
@@ -158,7 +180,7 @@ __device__ __forceinline__ const lds_char* stage_addr(uint32_t buf, int off) {
 }
 
 struct LaneOffsets {
-    int a, m, b0, b1;
+    int a, m, b0, b1, s;
 };
 
 __device__ __forceinline__ i32x8 read_b(uint32_t buf, const LaneOffsets& o, int j) {
@@ -167,29 +189,58 @@ __device__ __forceinline__ i32x8 read_b(uint32_t buf, const LaneOffsets& o, int 
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
-// The scales of one stage, as loaded: the lane's token of each fragment column, and the wave's rows.
+// The scales of one stage: the lane's token of each fragment column, and the wave's rows.
 struct Scales {
     uint32_t x[FN], w;
 };
+
+// Scales of X, CHUNK stages at a time, into one of two LDS areas: a byte load a stage would bring a line of every token
+// through L1 each time, which the operands' traffic has emptied by then (8192^3: 460 us). Words
+// [token / 8][stage % CHUNK][token % 8]: lane i of a load takes stage i / 8 of token 8 t + i % 8.
+__device__ __forceinline__ void load_chunk(uint32_t lds, const Args& a, const Desc& d, int s, int wave, int lane) {
+    const i32x4 rS = make_rsrc(d.xs, d.xs_bytes);
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+        const int t = 4 * wave + h;
+        dma1(lds + t * 256, (uint32_t)((8 * t + (lane & 7)) * (int)a.lds + s + (lane >> 3)), rS);
+    }
+}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, bytes, 0x00020000);
 }
 
-__device__ __forceinline__ Scales load_scales(const Args& a, const Desc& d, const uint32_t (&off)[FN], int s) {
-    Scales r;
-    const __amdgpu_buffer_rsrc_t rs = rsrc(d.xs, d.xs_bytes);
+// The wave's weight scale of stage s of tile d; rows past M read zero.
+__device__ __forceinline__ uint32_t load_w(const Args& a, const Desc& d, int s) {
     const __amdgpu_buffer_rsrc_t rw = rsrc(a.ws, (int)((a.M + 127) / 128 * a.S));  // below 2^28 (M <= 2^22, K <= 2^20)
-#pragma unroll
-    for (int j = 0; j < FN; j++) r.x[j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)off[j], s, 0);
-    r.w = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rw, d.wrow, s, 0);
-    return r;
+    return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rw, d.wrow, s, 0);
 }
 
-__device__ __forceinline__ void factors(const Scales& s, float (&f)[FN]) {
-    const int w = (int)s.w - 127;
+// The running units of a lane's four tokens: exponents of the current and of the largest unit (biases included), and
+// the stage's factors 2^(previous - current).
+struct Units {
+    int e[FN], top[FN];
+    float f[FN];
+    uint32_t skip;  // bit j: column j's block is left out
+};
+
+__device__ __forceinline__ void reset(Units& u) {
 #pragma unroll
-    for (int j = 0; j < FN; j++) f[j] = __builtin_amdgcn_ldexpf(scale_value(s.x[j]), w);
+    for (int j = 0; j < FN; j++) u.e[j] = u.top[j] = 0;
+}
+
+__device__ __forceinline__ void advance(Units& u, const Scales& s) {
+    u.skip = 0;
+#pragma unroll
+    for (int j = 0; j < FN; j++) {
+        const int e = (int)(s.x[j] + s.w);
+        u.top[j] = e > u.top[j] ? e : u.top[j];
+        const int least = u.top[j] - 64, now = e > least ? e : least;
+        u.skip |= (uint32_t)(e < least) << j;
+        const int d = u.e[j] - now + 127;  // at most 64 + 127
+        u.f[j] = s.x[j] == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(d > 0 ? d : 0) << 23);
+        u.e[j] = now;
+    }
 }
 
 struct AFrags {
@@ -197,23 +248,129 @@ struct AFrags {
     uint32_t idx[FM];
 };
 
-__device__ __forceinline__ f32x4 product(const AFrags& fa, int i, const i32x8& b) {
-    return __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(fa.a[i], b, f32x4{0.f, 0.f, 0.f, 0.f}, (int)fa.idx[i], 0, 0);
-}
-__device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& p, float f) {
+__device__ __forceinline__ void rescale(f32x4& acc, float f) {
 #pragma unroll
-    for (int e = 0; e < 4; e++) acc[e] = fmaf(p[e], f, acc[e]);
+    for (int e = 0; e < 4; e++) acc[e] *= f;
 }
 
-__device__ __forceinline__ void column(f32x4 (&acc)[FM][FN], const AFrags& fa, const i32x8& b, int j, float f) {
+__device__ __forceinline__ void multiply(f32x4& c, const AFrags& fa, int i, const i32x8& b) {
+    c = __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(fa.a[i], b, c, (int)fa.idx[i], 0, 0);
+}
+
+// Columns 0 and 1 of a stage, one after the other; each fragment is rescaled while the one before is multiplied.
+template <int J>
+__device__ __forceinline__ void column(f32x4 (&acc)[FM][FN], const AFrags& fa, const i32x8& b, const Units& u) {
 #pragma unroll
-    for (int i = 0; i < FM; i++) add_scaled(acc[i][j], product(fa, i, b), f);
+    for (int i = 0; i < FM; i++) {
+        if (i + 1 < FM) rescale(acc[i + 1][J], u.f[J]);
+        else rescale(acc[0][J + 1], u.f[J + 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(acc[i][J], fa, i, b);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// Columns 2 and 3 together, row block by row block; with RELOAD each A fragment is then replaced by the next stage's (at
+// pa, pm), so that these reads spread over half a stage.
+template <bool RELOAD>
+__device__ __forceinline__ void last_columns(f32x4 (&acc)[FM][FN], AFrags& fa, const i32x8& b2, const i32x8& b3,
+                                             const Units& u, const lds_char* pa, const lds_char* pm) {
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+        rescale(acc[i][3], u.f[3]);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(acc[i][2], fa, i, b2);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < FM) rescale(acc[i + 1][2], u.f[2]);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(acc[i][3], fa, i, b3);
+        if constexpr (RELOAD) {
+            fa.a[i] = *reinterpret_cast<lds_i32x4*>(pa + i * 1024);
+            fa.idx[i] = *reinterpret_cast<lds_u32*>(pm + i * 256);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+__device__ __forceinline__ void read_a(uint32_t buf, const LaneOffsets& o, AFrags& fa) {
+    const lds_char *pa = stage_addr(buf, o.a), *pm = stage_addr(buf, o.m);
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+        fa.a[i] = *reinterpret_cast<lds_i32x4*>(pa + i * 1024);
+        fa.idx[i] = *reinterpret_cast<lds_u32*>(pm + i * 256);
+    }
+}
+
+// What a wave holds of a stage between its parts.
+struct Stage {
+    AFrags fa;
+    i32x8 b0, b1, b2;
+    Scales sc;
+    Units u;
+    int chunk;  // LDS area of the current chunk of scales
+};
+
+// Zeroes the codes of tokens whose block is left out in column j.
+__device__ __forceinline__ void skip(i32x8& b, uint32_t mask, int j) {
+    const int keep = (int)((mask >> j) & 1u) - 1;
+#pragma unroll
+    for (int w = 0; w < 8; w++) b[w] &= keep;
+}
+
+__device__ __forceinline__ void read_x_scales(uint32_t area, int off, int s, Scales& sc) {
+    const lds_char* p = stage_addr(area + (uint32_t)(s & (CHUNK - 1)) * 32u, off);
+#pragma unroll
+    for (int j = 0; j < FN; j++) sc.x[j] = *reinterpret_cast<lds_u32*>(p + 512 * j);
+}
+
+// Stage s of the current tile from buffer `buf`; its A fragments, first two B columns and scales have been read. Before
+// the last two columns the barrier publishes the next stage's buffer and the loads of stage s + 2 (or the next
+// tile's) go into this one; a chunk's first stage fetches the next chunk's scales. NEXT: the next stage's operands are
+// read in the last two columns; a tile's last stage leaves that to after the epilogue, which needs the registers.
+template <int BN, bool NEXT>
+__device__ __forceinline__ void stage(const Args& a, const Desc& dc, const Desc& dn, int s, uint32_t l0, int buf,
+                                      f32x4 (&acc)[FM][FN], Stage& g, const LaneOffsets& o, int wave, int lane,
+                                      const LoadOffsets& lo) {
+    constexpr int STAGE_BYTES = Cfg<BN>::STAGE_BYTES, CHUNK_BYTES = Cfg<BN>::CHUNK_BYTES;
+    const uint32_t cb = l0 + buf * STAGE_BYTES, nb = l0 + (buf ^ 1) * STAGE_BYTES, chunks = l0 + NBUF * STAGE_BYTES;
+    const int S = a.S;
+    if ((s & (CHUNK - 1)) == 0) {
+        const bool in = s + CHUNK < S;
+        load_chunk(chunks + (g.chunk ^ 1) * CHUNK_BYTES, a, in ? dc : dn, in ? s + CHUNK : 0, wave, lane);
+    }
+    advance(g.u, g.sc);
+    g.sc.w = load_w(a, NEXT ? dc : dn, NEXT ? s + 1 : 0);  // landed by the wait below
+    g.b2 = read_b(cb, o, 3);
+    if (__builtin_amdgcn_ballot_w64(g.u.skip & 3u)) skip(g.b0, g.u.skip, 0), skip(g.b1, g.u.skip, 1);
+    rescale(acc[0][0], g.u.f[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    column<0>(acc, g.fa, g.b0, g.u);
+    g.b0 = read_b(cb, o, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    column<1>(acc, g.fa, g.b1, g.u);
+    wait_lgkmcnt0();  // this wave's reads of the stage are done
+    wait_vmcnt0();    // the next stage has landed
+    __builtin_amdgcn_s_barrier();
+    const bool here = s + NBUF < S;
+    load_stage<BN>(cb, a, here ? dc : dn, here ? s + NBUF : s + NBUF - S, wave, lo);
+    if (!NEXT || ((s + 1) & (CHUNK - 1)) == 0) g.chunk ^= 1;
+    read_x_scales(chunks + g.chunk * CHUNK_BYTES, o.s, NEXT ? s + 1 : 0, g.sc);
+    if (__builtin_amdgcn_ballot_w64(g.u.skip & 12u)) skip(g.b0, g.u.skip, 2), skip(g.b2, g.u.skip, 3);
+    if constexpr (NEXT) {
+        g.b1 = read_b(nb, o, 0);
+        last_columns<true>(acc, g.fa, g.b0, g.b2, g.u, stage_addr(nb, o.a), stage_addr(nb, o.m));
+        g.b0 = g.b1;
+        g.b1 = read_b(nb, o, 1);
+    } else {
+        last_columns<false>(acc, g.fa, g.b0, g.b2, g.u, nullptr, nullptr);
+    }
 }
 
 // Token-major epilogue from registers: each accumulator is 4 consecutive outputs of token row n. A quad transpose
 // across four row fragments gives each lane quad one token row, so a store instruction covers 16 rows x 64 outputs.
 template <bool F16, bool FULL>
-__device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Args& a, int64_t mw, int64_t nw, int lane) {
+__device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Units& u, const Args& a, int64_t mw,
+                                           int64_t nw, int lane) {
     const int q = lane >> 4, r = lane & 15, x = r & 3, c = r >> 2;
     uint16_t* const Y = static_cast<uint16_t*>(a.Y);
 #pragma unroll
@@ -223,7 +380,9 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Arg
             uint32_t v[4][2];
 #pragma unroll
             for (int f = 0; f < 4; f++) {
-                const f32x4 y = acc[4 * ig + f][j];
+                f32x4 y = acc[4 * ig + f][j];
+#pragma unroll
+                for (int e = 0; e < 4; e++) y[e] = __builtin_amdgcn_ldexpf(y[e], u.e[j] - 254);
                 v[f][0] = pack16<F16>(y[0], y[1]);
                 v[f][1] = pack16<F16>(y[2], y[3]);
             }
@@ -244,89 +403,70 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Arg
         }
 }
 
-template <bool F16>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemm_fp8_tiled_kernel(Args a) {
-    __shared__ __attribute__((aligned(16))) char smem[NBUF * STAGE_BYTES];
+template <int BN, bool F16>
+__global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemm_fp8_tiled_kernel(Args a) {
+    constexpr int STAGE_BYTES = Cfg<BN>::STAGE_BYTES;
+    __shared__ __attribute__((aligned(16))) char smem[Cfg<BN>::LDS_BYTES];
     const uint32_t l0 = (uint32_t)(size_t)(lds_char*)smem;
     const int p = blockIdx.x, S = a.S;
-    Tile cur = tile_of(a, p, 0);
+    Tile cur = tile_of<BN>(a, p, 0);
     if (!cur.valid) return;  // whole workgroup
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int wm0 = (wave >> 1) * WM, wn0 = (wave & 1) * WN;
+    const int wm0 = (wave & 1) * WM, wn0 = (wave >> 1) * WN;
     const LoadOffsets lo = load_offsets(a, lane);
     LaneOffsets o;
     o.a = (wm0 >> 4) * 1024 + lane * 16;
     o.m = A_BYTES + (wm0 >> 4) * 256 + lane * 4;
     o.b0 = A_BYTES + META_BYTES + (wn0 + r) * 128 + 16 * (q ^ swz(r));
     o.b1 = A_BYTES + META_BYTES + (wn0 + r) * 128 + 16 * (q ^ swz(r) ^ 4);
-    uint32_t so[FN];
-#pragma unroll
-    for (int j = 0; j < FN; j++) so[j] = (uint32_t)((wn0 + 16 * j + r) * (int)a.lds);
+    o.s = ((wn0 + r) >> 3) * 256 + (r & 7) * 4;
+
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; i++)
 #pragma unroll
         for (int j = 0; j < FN; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    Tile next = tile_of(a, p, 1);
-    Desc dc = desc_of(a, cur, wave, wm0), dn = desc_of(a, next, wave, wm0);
-    load_stage(l0, a, dc, 0, wave, lo);
-    Scales sc = load_scales(a, dc, so, 0);
+    Tile next = tile_of<BN>(a, p, 1);
+    Desc dc = desc_of<BN>(a, cur, wave, wm0), dn = desc_of<BN>(a, next, wave, wm0);
+    load_stage<BN>(l0, a, dc, 0, wave, lo);
+    Stage g;
+    g.chunk = 0;
+    load_chunk(l0 + NBUF * STAGE_BYTES, a, dc, 0, wave, lane);
+    g.sc.w = load_w(a, dc, 0);
     wait_vmcnt0();
     __builtin_amdgcn_s_barrier();
-    if (S > 1) load_stage(l0 + STAGE_BYTES, a, dc, 1, wave, lo);  // with one stage a workgroup has one tile
-    float f[FN];
-    factors(sc, f);
+    if (S > 1) load_stage<BN>(l0 + STAGE_BYTES, a, dc, 1, wave, lo);  // with one stage a workgroup has one tile
+    reset(g.u);
+    read_x_scales(l0 + NBUF * STAGE_BYTES, o.s, 0, g.sc);
 
     int buf = 0;
     for (int k = 1;; k++) {
-        for (int s = 0; s < S; s++, buf ^= 1) {
-            const uint32_t cb = l0 + buf * STAGE_BYTES;
-            // scales of the next stage (of the next tile after the last), landed by the wait below
-            sc = load_scales(a, s + 1 < S ? dc : dn, so, s + 1 < S ? s + 1 : 0);
-            AFrags fa;
-            const lds_char *pa = stage_addr(cb, o.a), *pm = stage_addr(cb, o.m);
-#pragma unroll
-            for (int i = 0; i < FM; i++) {
-                fa.a[i] = *reinterpret_cast<lds_i32x4*>(pa + i * 1024);
-                fa.idx[i] = *reinterpret_cast<lds_u32*>(pm + i * 256);
-            }
-            i32x8 b0 = read_b(cb, o, 0), b1 = read_b(cb, o, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            column(acc, fa, b0, 0, f[0]);
-            b0 = read_b(cb, o, 2);
-            __builtin_amdgcn_sched_barrier(0);
-            column(acc, fa, b1, 1, f[1]);
-            b1 = read_b(cb, o, 3);
-            __builtin_amdgcn_sched_barrier(0);
-            wait_lgkmcnt0();  // this wave's reads of the stage are done
-            wait_vmcnt0();    // the next stage has landed
-            __builtin_amdgcn_s_barrier();
-            const bool here = s + NBUF < S;
-            load_stage(cb, a, here ? dc : dn, here ? s + NBUF : s + NBUF - S, wave, lo);
-            column(acc, fa, b0, 2, f[2]);
-            column(acc, fa, b1, 3, f[3]);
-            factors(sc, f);
-        }
+        read_a(l0 + buf * STAGE_BYTES, o, g.fa);
+        g.b0 = read_b(l0 + buf * STAGE_BYTES, o, 0);
+        g.b1 = read_b(l0 + buf * STAGE_BYTES, o, 1);
+        for (int s = 0; s < S - 1; s++, buf ^= 1) stage<BN, true>(a, dc, dn, s, l0, buf, acc, g, o, wave, lane, lo);
+        stage<BN, false>(a, dc, dn, S - 1, l0, buf, acc, g, o, wave, lane, lo);
+        buf ^= 1;
         const int64_t mw = cur.m0 + wm0, nw = cur.n0 + wn0;
-        if (mw + WM <= a.M && nw + WN <= a.N && a.y_vec) store_tile<F16, true>(acc, a, mw, nw, lane);
-        else store_tile<F16, false>(acc, a, mw, nw, lane);
+        if (mw + WM <= a.M && nw + WN <= a.N && a.y_vec) store_tile<F16, true>(acc, g.u, a, mw, nw, lane);
+        else store_tile<F16, false>(acc, g.u, a, mw, nw, lane);
         if (!next.valid) break;
 #pragma unroll
         for (int i = 0; i < FM; i++)
 #pragma unroll
             for (int j = 0; j < FN; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        reset(g.u);
         cur = next;
         dc = dn;
-        next = tile_of(a, p, k + 1);
-        dn = desc_of(a, next, wave, wm0);
+        next = tile_of<BN>(a, p, k + 1);
+        dn = desc_of<BN>(a, next, wave, wm0);
     }
     wait_vmcnt0();  // the zero-filling loads past the last tile have landed before the workgroup ends
 }
 
-}  // namespace
-
-hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s) {
+template <int BN>
+hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
     Args a;
     a.values = g.values; a.meta = g.meta; a.ws = g.ws; a.X = g.X; a.xs = g.xs; a.Y = g.Y;
     a.M = g.M; a.K = g.K; a.N = g.N; a.ldx = g.ldx; a.lds = g.lds; a.ldy = g.ldy;
@@ -335,13 +475,20 @@ hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s) {
     a.tilesN = (int)((g.N + BN - 1) / BN);
     a.y_vec = g.ldy % 4 == 0;  // Y is 16-byte aligned
     const int64_t T = (int64_t)a.tilesM * a.tilesN;
-    // two workgroups a compute unit walking their tiles; one tile each where a tile has a single stage (the pipeline
-    // across tiles needs both buffers within one tile)
-    const int cus = device_cus();
-    const unsigned grid = (unsigned)(a.S >= NBUF && T > 2 * cus ? 2 * cus : T);
-    if (g.out_fp16) hipLaunchKernelGGL((gemm_fp8_tiled_kernel<true>), dim3(grid), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((gemm_fp8_tiled_kernel<false>), dim3(grid), dim3(256), 0, s, a);
+    // as many workgroups as fit walk the tiles; one tile each where a tile has a single stage (the pipeline across
+    // tiles needs both buffers within one tile)
+    const int fit = (BN == 128 ? 2 : 1) * device_cus();
+    const dim3 grid((unsigned)(a.S >= NBUF && T > fit ? fit : T)), block(64 * Cfg<BN>::WAVES);
+    if (g.out_fp16) hipLaunchKernelGGL((gemm_fp8_tiled_kernel<BN, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((gemm_fp8_tiled_kernel<BN, false>), grid, block, 0, s, a);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s) {
+    if (((g.M + BM - 1) / BM) * ((g.N + 255) / 256) >= device_cus()) return launch<256>(g, s);
+    return launch<128>(g, s);
 }
 
 }  // namespace sp24
