@@ -38,6 +38,10 @@ constexpr int CHUNK = 8;  // stages whose scales are fetched together
 template <int BN_>
 struct Cfg {
     static constexpr int BN = BN_, WAVES = BN_ / 32;
+    // whether a stage's loads are spread over the matrix instructions after the barrier (28672 x 8192 x 8192:
+    // 1379 us against 1414 us in one burst) or issued at once (128 wide, two workgroups a compute unit: 11008 x 4096 at
+    // N = 512 35.5 us against 40 us spread)
+    static constexpr bool SPREAD = BN == 256;
     static constexpr int STAGE_BYTES = A_BYTES + META_BYTES + BN * BK;
     static constexpr int CHUNK_BYTES = BN * CHUNK * 4;  // a word for each scale
     static constexpr int LDS_BYTES = NBUF * STAGE_BYTES + 2 * CHUNK_BYTES;
@@ -152,21 +156,35 @@ __device__ __forceinline__ LoadOffsets load_offsets(const Args& a, int lane) {
     return o;
 }
 
+// The loads of one stage, to be issued one by one (0 .. COUNT - 1) or at once.
 template <int BN>
-__device__ __forceinline__ void load_stage(uint32_t lds, const Args& a, const Desc& d, int s, int wave, const LoadOffsets& lo) {
-    constexpr int AL = 16 / Cfg<BN>::WAVES;
-#pragma unroll
-    for (int j = 0; j < AL; j++) {
-        const int b = AL * wave + j;
-        dma16(lds + b * 1024, lo.a + (uint32_t)(b * a.S + s) * 1024u, d.rA);
+struct StageLoads {
+    static constexpr int AL = 16 / Cfg<BN>::WAVES, COUNT = AL + 5;
+    static_assert(!Cfg<BN>::SPREAD || COUNT <= FM, "one load a row block");
+    uint32_t lds;
+    i32x4 rA, rM, rB;
+    int s, left, S, wave;
+
+    __device__ __forceinline__ StageLoads(uint32_t lds_, const Args& a, const Desc& d, int s_, int wave_)
+        : lds(lds_), rA(d.rA), rM(d.rM), s(s_), left((int)a.K - s_ * BK), S(a.S), wave(wave_) {
+        rB = make_rsrc(d.x + s * BK, d.xbytes - s * BK);
     }
-    if (AL == 4 || wave < 4) dma16(lds + A_BYTES + 4 * wave * 256, lo.m + (uint32_t)(4 * wave * a.S + s) * 256u, d.rM);
-    const int k0 = s * BK, left = (int)a.K - k0;
-    const i32x4 rB = make_rsrc(d.x + k0, d.xbytes - k0);
+    __device__ __forceinline__ void issue(int n, const LoadOffsets& lo) const {
+        if (n < AL) {
+            const int b = AL * wave + n;
+            dma16(lds + b * 1024, lo.a + (uint32_t)(b * S + s) * 1024u, rA);
+        } else if (n == AL) {
+            if (AL == 4 || wave < 4) dma16(lds + A_BYTES + 4 * wave * 256, lo.m + (uint32_t)(4 * wave * S + s) * 256u, rM);
+        } else {
+            const int h = n - AL - 1;
+            dma16(lds + A_BYTES + META_BYTES + (32 * wave + 8 * h) * 128, lo.unit[h & 1] < left ? lo.b[h] : OOR, rB);
+        }
+    }
+    __device__ __forceinline__ void issue_all(const LoadOffsets& lo) const {
 #pragma unroll
-    for (int h = 0; h < 4; h++)
-        dma16(lds + A_BYTES + META_BYTES + (32 * wave + 8 * h) * 128, lo.unit[h & 1] < left ? lo.b[h] : OOR, rB);
-}
+        for (int n = 0; n < COUNT; n++) issue(n, lo);
+    }
+};
 
 typedef __attribute__((address_space(3))) char lds_char;
 typedef const __attribute__((address_space(3))) i32x4 lds_i32x4;
@@ -272,11 +290,13 @@ __device__ __forceinline__ void column(f32x4 (&acc)[FM][FN], const AFrags& fa, c
 
 // Columns 2 and 3 together, row block by row block; with RELOAD each A fragment is then replaced by the next stage's (at
 // pa, pm), so that these reads spread over half a stage.
-template <bool RELOAD>
-__device__ __forceinline__ void last_columns(f32x4 (&acc)[FM][FN], AFrags& fa, const i32x8& b2, const i32x8& b3,
+template <int BN, bool RELOAD>
+__device__ __forceinline__ void last_columns(const StageLoads<BN>& loads, const LoadOffsets& lo, f32x4 (&acc)[FM][FN], AFrags& fa, const i32x8& b2, const i32x8& b3,
                                              const Units& u, const lds_char* pa, const lds_char* pm) {
 #pragma unroll
     for (int i = 0; i < FM; i++) {
+        if constexpr (Cfg<BN>::SPREAD)
+            if (i < StageLoads<BN>::COUNT) loads.issue(i, lo);
         rescale(acc[i][3], u.f[3]);
         __builtin_amdgcn_sched_barrier(0);
         multiply(acc[i][2], fa, i, b2);
@@ -352,17 +372,18 @@ __device__ __forceinline__ void stage(const Args& a, const Desc& dc, const Desc&
     wait_vmcnt0();    // the next stage has landed
     __builtin_amdgcn_s_barrier();
     const bool here = s + NBUF < S;
-    load_stage<BN>(cb, a, here ? dc : dn, here ? s + NBUF : s + NBUF - S, wave, lo);
+    const StageLoads<BN> loads(cb, a, here ? dc : dn, here ? s + NBUF : s + NBUF - S, wave);
+    if constexpr (!Cfg<BN>::SPREAD) loads.issue_all(lo);
     if (!NEXT || ((s + 1) & (CHUNK - 1)) == 0) g.chunk ^= 1;
     read_x_scales(chunks + g.chunk * CHUNK_BYTES, o.s, NEXT ? s + 1 : 0, g.sc);
     if (__builtin_amdgcn_ballot_w64(g.u.skip & 12u)) skip(g.b0, g.u.skip, 2), skip(g.b2, g.u.skip, 3);
     if constexpr (NEXT) {
         g.b1 = read_b(nb, o, 0);
-        last_columns<true>(acc, g.fa, g.b0, g.b2, g.u, stage_addr(nb, o.a), stage_addr(nb, o.m));
+        last_columns<BN, true>(loads, lo, acc, g.fa, g.b0, g.b2, g.u, stage_addr(nb, o.a), stage_addr(nb, o.m));
         g.b0 = g.b1;
         g.b1 = read_b(nb, o, 1);
     } else {
-        last_columns<false>(acc, g.fa, g.b0, g.b2, g.u, nullptr, nullptr);
+        last_columns<BN, false>(loads, lo, acc, g.fa, g.b0, g.b2, g.u, nullptr, nullptr);
     }
 }
 
@@ -429,14 +450,14 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
 
     Tile next = tile_of<BN>(a, p, 1);
     Desc dc = desc_of<BN>(a, cur, wave, wm0), dn = desc_of<BN>(a, next, wave, wm0);
-    load_stage<BN>(l0, a, dc, 0, wave, lo);
+    StageLoads<BN>(l0, a, dc, 0, wave).issue_all(lo);
     Stage g;
     g.chunk = 0;
     load_chunk(l0 + NBUF * STAGE_BYTES, a, dc, 0, wave, lane);
     g.sc.w = load_w(a, dc, 0);
     wait_vmcnt0();
     __builtin_amdgcn_s_barrier();
-    if (S > 1) load_stage<BN>(l0 + STAGE_BYTES, a, dc, 1, wave, lo);  // with one stage a workgroup has one tile
+    if (S > 1) StageLoads<BN>(l0 + STAGE_BYTES, a, dc, 1, wave).issue_all(lo);  // with one stage a workgroup has one tile
     reset(g.u);
     read_x_scales(l0 + NBUF * STAGE_BYTES, o.s, 0, g.sc);
 
