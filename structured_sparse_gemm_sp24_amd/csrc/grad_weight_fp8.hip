@@ -16,6 +16,7 @@
 // the workspace, and a second kernel adds the parts in order.
 #include "fp8_device.h"
 #include "sp24_launch.h"
+#include "grad_weight_fp8.h"
 
 namespace sp24 {
 namespace {
@@ -33,22 +34,11 @@ struct Args {
 
 __device__ __forceinline__ int swz(int n) { return 2 * (n & 3) + ((n >> 3) & 1); }
 
-// Whether position e (0..3) of the group at column k of row m is kept: bit e of the result.
-__device__ __forceinline__ uint32_t kept_bits(const uint8_t* meta, int64_t m, int64_t k, int64_t tiles) {
-    const uint32_t byte = meta[tiled_offset<16>(m, k >> 3, tiles)];
-    const uint32_t nib = (k & 4) ? byte >> 4 : byte & 15u;
-    return (1u << (nib & 3u)) | (1u << (nib >> 2));
-}
-
 // Four consecutive k of row m of the result.
 template <bool F32>
 __device__ __forceinline__ void store4(char* out, int64_t ldw, int64_t m, int64_t k, f32x4 v, const uint8_t* meta,
                                        int64_t tiles) {
-    if (meta) {
-        const uint32_t keep = kept_bits(meta, m, k, tiles);
-#pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = (keep >> e) & 1u ? v[e] : 0.f;
-    }
+    if (meta) v = masked(v, meta, m, k, tiles);
     if constexpr (F32) *reinterpret_cast<f32x4*>(out + (m * ldw + k) * 4) = v;
     else *reinterpret_cast<u32x2*>(out + (m * ldw + k) * 2) = u32x2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
 }
@@ -182,6 +172,7 @@ int grad_weight_parts(int64_t M, int64_t K, int64_t N) {
 }
 
 hipError_t launch_grad_weight(const Fp8GradArgs& g, hipStream_t s) {
+    if (((g.M + 255) / 256) * ((g.K + 255) / 256) >= 200) return launch_grad_weight_tiled(g, s);
     const int parts = grad_weight_parts(g.M, g.K, g.N);
     Args a;
     a.dY = static_cast<const char*>(g.dY); a.X = g.X; a.xs = g.xs;

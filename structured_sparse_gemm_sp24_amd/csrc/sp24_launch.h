@@ -122,5 +122,6 @@ struct Fp8GradArgs {
 // Parts that the tokens are split into; with more than one the workspace holds an M x K fp32 matrix for each.
 int grad_weight_parts(int64_t M, int64_t K, int64_t N);
 hipError_t launch_grad_weight(const Fp8GradArgs& g, hipStream_t s);
+hipError_t launch_grad_weight_tiled(const Fp8GradArgs& g, hipStream_t s);
 
 }  // namespace sp24

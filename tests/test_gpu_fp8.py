@@ -391,7 +391,8 @@ def test_gemm_counts_kept_weights():
 # ---------------------------------------------------------------- the weight's gradient
 
 GRAD_SIZES = [(1, 1, 16), (2, 17, 128), (31, 128, 144), (32, 130, 272), (33, 8, 48), (65, 300, 400), (300, 257, 640),
-              (2000, 130, 144), (6304, 136, 256), (1000, 768, 768), (64, 4100, 528), (513, 1024, 2064)]
+              (2000, 130, 144), (6304, 136, 256), (1000, 768, 768), (64, 4100, 528), (513, 1024, 2064),
+              (1, 4096, 4096), (70, 3601, 3600), (129, 4104, 3856), (700, 3330, 4112)]
 
 
 @pytest.mark.parametrize("masked", [False, True])
