@@ -90,15 +90,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const bool xk = k0 + 16 * xu < a.K;
     const uint32_t xo = xk ? (uint32_t)(xt * (int)a.ldx + 16 * xu) : OOR;
     const uint32_t so = xk ? (uint32_t)(xt * (int)a.lds + (xu >> 3)) : OOR;
-    auto load_codes = [&](int s, Codes& c) {
+    struct CodeSource {
+        __amdgpu_buffer_rsrc_t x, s;
+    };
+    auto code_source = [&](int s) {
         const int64_t n = (int64_t)s * BN;
-        const __amdgpu_buffer_rsrc_t rx = rsrc(a.X + n * a.ldx + k0, s < S ? (a.N - 1 - n) * a.ldx + a.K - k0 : 0);
-        const __amdgpu_buffer_rsrc_t rs = rsrc(a.xs + n * a.lds + (k0 >> 7), s < S ? (a.N - 1 - n) * a.lds + (a.K + 127) / 128 - (k0 >> 7) : 0);
-#pragma unroll
-        for (int h = 0; h < 4; h++) {
-            c.x[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(xo + (xk ? 16u * h * (uint32_t)a.ldx : 0u)), 0, 0));
-            c.s[h] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)(so + (xk ? 16u * h * (uint32_t)a.lds : 0u)), 0, 0);
-        }
+        return CodeSource{rsrc(a.X + n * a.ldx + k0, s < S ? (a.N - 1 - n) * a.ldx + a.K - k0 : 0),
+                          rsrc(a.xs + n * a.lds + (k0 >> 7), s < S ? (a.N - 1 - n) * a.lds + (a.K + 127) / 128 - (k0 >> 7) : 0)};
+    };
+    auto load_codes = [&](const CodeSource& src, int h, Codes& c) {
+        c.x[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(src.x, (int)(xo + (xk ? 16u * h * (uint32_t)a.ldx : 0u)), 0, 0));
+        c.s[h] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(src.s, (int)(so + (xk ? 16u * h * (uint32_t)a.lds : 0u)), 0, 0);
     };
     // dY: load h of a wave fills tokens 16 wave + 2 h, + 1; lane i the 16 bytes i % 32 of token i / 32, which belong to
     // unit (i % 32) / 2 ^ swz
@@ -108,26 +110,25 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         const int n = 2 * (v & 1) + 8 * (v >> 1) + (lane >> 5), u = ((lane & 31) >> 1) ^ swz(n);
         yo[v] = (uint32_t)(((lane >> 5) * (int)a.lddy + 16 * u + 8 * (lane & 1)) * 2);
     }
-    auto load_dy = [&](int s, uint32_t buf) {
+    auto dy_source = [&](int s) {
         const int64_t n = (int64_t)s * BN + 16 * wave;
         const int64_t bytes = ((a.N - 1 - n) * a.lddy + a.M - m0) * 2;
-        const i32x4 ry = make_rsrc(a.dY + (n * a.lddy + m0) * 2, s < S ? (bytes + 3) & ~(int64_t)3 : 0);
-#pragma unroll
-        for (int h = 0; h < 8; h++)
-            dma16(buf + HALF_BYTES + (16 * wave + 2 * h) * 512, yo[(h & 1) + 2 * (h >> 2)] + (uint32_t)(2 * h * (int)a.lddy * 2), ry);
+        return make_rsrc(a.dY + (n * a.lddy + m0) * 2, s < S ? (bytes + 3) & ~(int64_t)3 : 0);
     };
-    auto write_codes = [&](const Codes& c, int h, uint32_t buf) {
+    auto load_dy = [&](const i32x4& src, int h, uint32_t buf) {
+        dma16(buf + HALF_BYTES + (16 * wave + 2 * h) * 512, yo[(h & 1) + 2 * (h >> 2)] + (uint32_t)(2 * h * (int)a.lddy * 2), src);
+    };
+    // half e (8 codes) of unit h, as bf16
+    auto write_codes = [&](const Codes& c, int h, int e, uint32_t buf) {
         const int n = xt + 16 * h;
         const float s = scale_value(c.s[h]);
-        u32x4 w[2];
+        u32x4 w;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            w[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x[h][i], s, false));
-            w[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x[h][i], s, true));
+        for (int i = 0; i < 2; i++) {
+            w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x[h][2 * e + i], s, false));
+            w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x[h][2 * e + i], s, true));
         }
-        lds_u32x4* const p = (lds_u32x4*)(lds_char*)(size_t)(buf + n * 512 + ((xu ^ swz(n)) << 5));
-        p[0] = w[0];
-        p[1] = w[1];
+        *(lds_u32x4*)(lds_char*)(size_t)(buf + n * 512 + ((xu ^ swz(n)) << 5) + 16 * e) = w;
     };
 
     // the lane's place in a step's columns: row 8 q + r / 4, 8 bytes r % 4 of its 32-byte unit; unit c at c ^ swz(row)
@@ -145,15 +146,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         for (int j = 0; j < F; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     Codes c, next;
-    load_codes(0, c);
-    load_dy(0, l0);
-    load_codes(1, next);
-    __builtin_amdgcn_s_waitcnt(0x0F70);
+    {
+        const CodeSource c0 = code_source(0), c1 = code_source(1), c2 = code_source(2);
+        const i32x4 d0 = dy_source(0), d1 = dy_source(1);
 #pragma unroll
-    for (int h = 0; h < 4; h++) write_codes(c, h, l0);
-    c = next;
-    load_dy(1, l0 + STAGE_BYTES);
-    load_codes(2, next);
+        for (int h = 0; h < 4; h++) load_codes(c0, h, c);
+#pragma unroll
+        for (int h = 0; h < 8; h++) load_dy(d0, h, l0);
+#pragma unroll
+        for (int h = 0; h < 4; h++) load_codes(c1, h, next);
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+#pragma unroll
+        for (int h = 0; h < 4; h++) write_codes(c, h, 0, l0), write_codes(c, h, 1, l0);
+        c = next;
+#pragma unroll
+        for (int h = 0; h < 8; h++) load_dy(d1, h, l0 + STAGE_BYTES);
+#pragma unroll
+        for (int h = 0; h < 4; h++) load_codes(c2, h, next);
+    }
     __syncthreads();
 
     bf16x8 x[F], y0[F], y1[F];  // an x fragment is replaced by the next step's after its row of products
@@ -163,30 +173,41 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     uint32_t cur = l0, oth = l0 + STAGE_BYTES;
 #pragma unroll 1
     for (int s = 0; s < S; s++) {
-        // step 0, with the fragments of step 1 and the codes of the next stage
+        // step 0, with the fragments of step 1 and the codes of the next stage. The matrix unit is busy for four issue
+        // slots of an instruction, so a wave alone on its SIMD keeps it fed only if no more than three others stand
+        // between two of them: the side work is dealt out in such pieces.
 #pragma unroll
-        for (int i = 0; i < F; i++) {
-            y1[i] = frag(cur + py[i] + 32 * 512);
-            if (i & 1) write_codes(c, i >> 1, oth);
+        for (int i = 0; i < F; i++)
 #pragma unroll
-            for (int j = 0; j < F; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y0[j], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            x[i] = frag(cur + px[i] + 32 * 512);
-        }
+            for (int j = 0; j < F; j++) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y0[j], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (j == 0) y1[i] = frag(cur + py[i] + 32 * 512);
+                if (j == 2 && i > 0) x[i - 1] = frag(cur + px[i - 1] + 32 * 512);
+                if (j == 4) write_codes(c, i >> 1, i & 1, oth);
+            }
+        x[F - 1] = frag(cur + px[F - 1] + 32 * 512);
         __builtin_amdgcn_s_waitcnt(0x0070);  // every load and LDS access of this wave is done
         __builtin_amdgcn_s_barrier();
-        load_dy(s + 2, cur);
-        c = next;
-        load_codes(s + 3, next);
-        // step 1, with the fragments of the next stage's step 0
+        // step 1, with the fragments of the next stage's step 0 and the loads of stages s + 2 (dY) and s + 3 (codes)
+        const i32x4 dsrc = dy_source(s + 2);
+        const CodeSource csrc = code_source(s + 3);
 #pragma unroll
-        for (int i = 0; i < F; i++) {
-            y0[i] = frag(oth + py[i]);
+        for (int i = 0; i < F; i++)
 #pragma unroll
-            for (int j = 0; j < F; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y1[j], acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            x[i] = frag(oth + px[i]);
-        }
+            for (int j = 0; j < F; j++) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y1[j], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (j == 0) y0[i] = frag(oth + py[i]);
+                if (j == 2 && i > 0) x[i - 1] = frag(oth + px[i - 1]);
+                if (j == 4) load_dy(dsrc, i, cur);
+                if (j == 6 && i < 4) {
+                    c.x[i] = next.x[i];
+                    c.s[i] = next.s[i];
+                    load_codes(csrc, i, next);
+                }
+            }
+        x[F - 1] = frag(oth + px[F - 1]);
         const uint32_t t = cur;
         cur = oth;
         oth = t;
