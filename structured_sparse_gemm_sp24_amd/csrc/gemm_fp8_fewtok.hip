@@ -158,11 +158,32 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
 
 }  // namespace
 
+// Row blocks a workgroup (R), tiles a request (U) and waves (S), measured on MI355X with weights rotated beyond the
+// Infinity Cache (us):
+//  one fragment: 4096 x 4096 (256 row blocks) at N = 1 / 8 / 16: 4.4 / 5.0 / 5.9 with R = 1; 11008 x 4096 (688) at N = 1 /
+//    8: 8.7 / 9.0 with R = 2 against 8.5 / 10.4 with 1, at N = 16 10.1 with R = 4 against 12.8; 28672 x 8192 (1792) at N
+//    = 1 / 8: 29.4 / 31.1 with R = 2, at N = 16 33.0 with R = 8 against 35.5 with 4;
+//  two: 4096 x 4096 8.6 (R = 1) against 10.4; 11008 x 4096 12.4 (R = 4) against 15.6 (R = 2), 28672 x 8192 37.8 against 53.8;
+//  three: 4096 x 4096 11.3 (R = 1), 11008 x 4096 14.3 (R = 4), 28672 x 8192 47.8 (R = 4);
+//  four, and groups of 64 tokens: the largest R that still gives every compute unit a workgroup (4096 x 4096 at N = 64 14.4
+//    with R = 1 against 16.8 with 4, at N = 100 15.4 with 2, at N = 200 16.9 with 4 against 26.3 with 2).
+// The groups stream the weight once each, from L2 after the first; the tiled kernel reads it once but fills the chip
+// only with many tiles. Up to 2.25 workgroups of 64 x 64 a compute unit this one is the faster (4096 x 4096 at N = 512, 2:
+// 28.9 against 37 us; 11008 x 4096 at N = 200, 2.7: 40.7 against 38.8; 28672 x 8192 at N = 64, 1.75: 56 against 71, at N =
+// 100, 3.5: 89 against 75).
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s) {
-    if (g.N > 64) return launch_gemm_fp8_tiled(g, s);
-    if (g.N <= 16) return launch<1, 1, 2, 8>(g, s);
-    if (g.N <= 32) return launch<2, 2, 2, 8>(g, s);
-    return launch<4, 2, 2, 4>(g, s);
+    const int64_t nb = (g.M + 15) / 16, groups = (g.N + 63) / 64, cus = device_cus();
+    if (4 * ((nb + 3) / 4) * groups > 9 * cus && g.N > 64) return launch_gemm_fp8_tiled(g, s);
+    const bool small = nb <= 2 * cus;
+    if (g.N <= 16) {
+        if (small) return launch<1, 1, 4, 4>(g, s);
+        if (g.N <= 8) return launch<1, 2, 2, 4>(g, s);
+        return nb <= 4 * cus ? launch<1, 4, 4, 8>(g, s) : launch<1, 8, 2, 8>(g, s);
+    }
+    if (g.N <= 32) return small ? launch<2, 1, 2, 4>(g, s) : launch<2, 4, 1, 8>(g, s);
+    if (g.N <= 48) return small ? launch<3, 1, 2, 4>(g, s) : launch<3, 4, 2, 4>(g, s);
+    if (nb * groups <= cus) return launch<4, 1, 2, 4>(g, s);
+    return nb * groups <= 2 * cus ? launch<4, 2, 2, 4>(g, s) : launch<4, 4, 2, 4>(g, s);
 }
 
 }  // namespace sp24
