@@ -21,6 +21,14 @@ __device__ __forceinline__ Raw8<DT> load8(const char* p) {
     if constexpr (DT == T_FP32) r.w[1] = *reinterpret_cast<const u32x4*>(p + 16);
     return r;
 }
+// The same with the non-temporal hint, for rows that are read once.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8_once(const char* p) {
+    Raw8<DT> r;
+    r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    if constexpr (DT == T_FP32) r.w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 16));
+    return r;
+}
 template <int DT>
 __device__ __forceinline__ Raw8<DT> zero8() {
     Raw8<DT> r;

@@ -6,13 +6,13 @@
 // codes (v_cvt_scalef32_pk_bf16_fp8), done once an element while a tile is staged. Both operands have the summed
 // index n as their slow axis; ds_read_b64_tr_b16 transposes them on the way from LDS to registers.
 //
-// Workgroup tile: 128 (k) x 128 (m), four waves of 64 x 64, 32 tokens a stage. LDS rows (one token) are 256 bytes in 8
+// Workgroup tile: 128 (k) x 128 (m), four waves of 64 x 64, 64 tokens a stage. LDS rows (one token) are 256 bytes in 8
 // units of 32 bytes, unit u of row n at u ^ (2 (n & 3) + ((n >> 3) & 1)): the 16 rows of a transposing read
 // (8 q + {0..3} for q = 0..3, 32 bytes each) then fall in 8 distinct units, two rows in each.
 // A is x (rows k) and B is dY (columns m): an accumulator holds four consecutive k of one m, one 2:4 group, so a
 // group's mask is one nibble and a store is 16 bytes (8 for bf16).
 //
-// Where the weight has too few tiles for the chip, the tokens are split over grid.z; each part writes fp32 sums to
+// Where the weight has too few tiles for the chip, the tokens are split; each part writes fp32 sums to
 // the workspace, and a second kernel adds the parts in order.
 #include "fp8_device.h"
 #include "sp24_launch.h"
@@ -21,15 +21,17 @@
 namespace sp24 {
 namespace {
 
-constexpr int BT = 128, BN = 32;
+constexpr int BT = 128, BN = 64;
+constexpr int XH = BN / 32, YH = BN / 16;  // 16-byte loads of a thread in a stage: codes, dY
 
 struct Args {
     const char* dY;
     const uint8_t *X, *xs, *meta;
     char* out;
     int64_t N, M, K, lddy, ldx, lds, ldw;
-    int64_t per;  // tokens of a part, a multiple of BN
+    int64_t per;  // tokens of a part, a multiple of 2 BN
     int64_t part_stride;
+    int tiles, tilesK;
 };
 
 __device__ __forceinline__ int swz(int n) { return 2 * (n & 3) + ((n >> 3) & 1); }
@@ -43,9 +45,15 @@ __device__ __forceinline__ void store4(char* out, int64_t ldw, int64_t m, int64_
     else *reinterpret_cast<u32x2*>(out + (m * ldw + k) * 2) = u32x2{pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
 }
 
+constexpr uint32_t OOR = 0x80000000u;  // a byte offset past every record count, also with a row's offset added
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes, bool any) {
+    const int64_t n = !any ? 0 : (bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0ll : bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
+}
+
 struct Staged {
-    u32x4 x, y[2];
-    uint32_t s;
+    u32x4 x[XH], y[YH];
+    uint32_t s[XH];
 };
 
 template <bool F32>
@@ -53,56 +61,62 @@ __global__ __launch_bounds__(256) void grad_weight_kernel(Args a) {
     __shared__ __attribute__((aligned(16))) char sx[2][BN * 256];
     __shared__ __attribute__((aligned(16))) char sy[2][BN * 256];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, q = lane >> 4;
-    const int64_t k0 = (int64_t)blockIdx.x * BT, m0 = (int64_t)blockIdx.y * BT;
-    const int64_t n_lo = (int64_t)blockIdx.z * a.per, n_hi = n_lo + a.per < a.N ? n_lo + a.per : a.N;
+    const int part = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+    const int tk = tile % a.tilesK, tm = tile / a.tilesK;
+    const int64_t k0 = (int64_t)tk * BT, m0 = (int64_t)tm * BT;
+    const int64_t n_lo = (int64_t)part * a.per, n_hi = n_lo + a.per < a.N ? n_lo + a.per : a.N;
     const int wk = (wave >> 1) * 64, wm = (wave & 1) * 64;
 
-    // x: thread t takes 16 codes (unit t % 8) of token t / 8; dY: 8 elements (unit t % 16) of tokens t / 16 and +16
+    // x: thread t takes 16 codes (unit t % 8) of token t / 8; dY: 8 elements (unit t % 16) of tokens t / 16 and +16. Loads
+    // through descriptors and without branches, so that the compiler can count what is in flight: units past K, tokens
+    // past the part's end and elements past dY's end read zeros; elements past M inside a row feed sums that are not
+    // stored.
+    const bool xk = k0 + 16 * (tid & 7) < a.K;
+    const uint32_t xo = xk ? (uint32_t)((tid >> 3) * (int)a.ldx + 16 * (tid & 7)) : OOR;
+    const uint32_t so = xk ? (uint32_t)((tid >> 3) * (int)a.lds) : OOR;
+    const uint32_t yo = m0 + 8 * (tid & 15) < a.M ? (uint32_t)(((tid >> 4) * (int)a.lddy + 8 * (tid & 15)) * 2) : OOR;
     auto load = [&](int64_t n0) {
         Staged g;
-        const int64_t n = n0 + (tid >> 3), k = k0 + 16 * (tid & 7);
-        const bool ok = n < n_hi && k < a.K;
-        g.x = ok ? *reinterpret_cast<const u32x4*>(a.X + n * a.ldx + k) : u32x4{0, 0, 0, 0};
-        g.s = ok ? a.xs[n * a.lds + blockIdx.x] : 127u;
+        const int64_t left = n_hi - 1 - n0;  // descriptors of no bytes from n_hi on
+        const __amdgpu_buffer_rsrc_t rx = rsrc(a.X + n0 * a.ldx + k0, left * a.ldx + a.K - k0, left >= 0);
+        const __amdgpu_buffer_rsrc_t rs = rsrc(a.xs + n0 * a.lds + tk, left * a.lds + 1, left >= 0);
+        const __amdgpu_buffer_rsrc_t ry = rsrc(a.dY + (n0 * a.lddy + m0) * 2, ((left * a.lddy + a.M - m0) * 2 + 3) & ~(int64_t)3, left >= 0);
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const int64_t ny = n0 + (tid >> 4) + 16 * h, m = m0 + 8 * (tid & 15);
-            const char* p = a.dY + (ny * a.lddy + m) * 2;
-            u32x4 v = u32x4{0, 0, 0, 0};
-            if (ny < n_hi && m + 7 < a.M) {
-                v = *reinterpret_cast<const u32x4*>(p);
-            } else if (ny < n_hi) {
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    if (m + e < a.M) v[e >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
-            }
-            g.y[h] = v;
+        for (int h = 0; h < XH; h++) {
+            g.x[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(xo + 32u * h * (uint32_t)a.ldx), 0, 0));
+            g.s[h] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)(so + 32u * h * (uint32_t)a.lds), 0, 0);
         }
+#pragma unroll
+        for (int h = 0; h < YH; h++)
+            g.y[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, (int)(yo + 32u * h * (uint32_t)a.lddy), 0, 0));
         return g;
     };
     auto store = [&](const Staged& g, int buf) {
-        const int n = tid >> 3, u = tid & 7;
-        const float s = scale_value(g.s);
-        u32x4 w[2];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            w[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(g.x[i], s, false));
-            w[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(g.x[i], s, true));
+        for (int h = 0; h < XH; h++) {
+            const int n = (tid >> 3) + 32 * h, u = tid & 7;
+            const float s = scale_value(g.s[h]);
+            u32x4 w[2];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                w[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(g.x[h][i], s, false));
+                w[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(g.x[h][i], s, true));
+            }
+            char* const px = sx[buf] + n * 256 + ((u ^ swz(n)) << 5);
+            *reinterpret_cast<u32x4*>(px) = w[0];
+            *reinterpret_cast<u32x4*>(px + 16) = w[1];
         }
-        char* const px = sx[buf] + n * 256 + ((u ^ swz(n)) << 5);
-        *reinterpret_cast<u32x4*>(px) = w[0];
-        *reinterpret_cast<u32x4*>(px + 16) = w[1];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = 0; h < YH; h++) {
             const int ny = (tid >> 4) + 16 * h, uy = (tid & 15) >> 1;
             *reinterpret_cast<u32x4*>(sy[buf] + ny * 256 + ((uy ^ swz(ny)) << 5) + 16 * (tid & 1)) = g.y[h];
         }
     };
-    // fragment of 16 columns at c: lane (r, q) gets tokens 8 q .. 8 q + 7 of column c + r
+    // fragment of 16 columns at c in step t: lane (r, q) gets tokens 32 t + 8 q .. + 7 of column c + r
     const int row = 8 * q + (r >> 2), roff = row * 256 + 8 * (r & 3), rs = swz(row);
-    auto frag = [&](const char* base, int c) {
+    auto frag = [&](const char* base, int c, int t) {
         typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-        const char* p = base + roff + (((c >> 4) ^ rs) << 5);
+        const char* p = base + roff + t * (32 * 256) + (((c >> 4) ^ rs) << 5);
         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 4 * 256));
         typedef short i16x8 __attribute__((ext_vector_type(8)));
@@ -115,29 +129,36 @@ __global__ __launch_bounds__(256) void grad_weight_kernel(Args a) {
 #pragma unroll
         for (int j = 0; j < 4; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    int buf = 0;
-    if (n_lo < n_hi) {
-        store(load(n_lo), 0);
-        __syncthreads();
-        for (int64_t n0 = n_lo; n0 < n_hi; n0 += BN, buf ^= 1) {
-            const bool more = n0 + BN < n_hi;
-            Staged g;
-            if (more) g = load(n0 + BN);
+    // Stage n0 from buffer `buf`: `use` holds the next stage's operands, loaded a stage ago, `next` takes those of the one
+    // after it. The two alternate without copies, which would wait for the loads just issued.
+    auto step = [&](int64_t n0, int buf, const Staged& use, Staged& next) {
+        next = load(n0 + 2 * BN);  // zeros from n_hi on
+#pragma unroll
+        for (int t = 0; t < BN / 32; t++) {
             bf16x8 fx[4], fy[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) fx[i] = frag(sx[buf], wk + 16 * i);
+            for (int i = 0; i < 4; i++) fx[i] = frag(sx[buf], wk + 16 * i, t);
 #pragma unroll
-            for (int j = 0; j < 4; j++) fy[j] = frag(sy[buf], wm + 16 * j);
+            for (int j = 0; j < 4; j++) fy[j] = frag(sy[buf], wm + 16 * j, t);
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[i], fy[j], acc[i][j], 0, 0, 0);
-            if (more) store(g, buf ^ 1);
-            __syncthreads();
+        }
+        store(use, buf ^ 1);
+        __syncthreads();
+    };
+    if (n_lo < n_hi) {
+        Staged g0 = load(n_lo), g1 = load(n_lo + BN);
+        store(g0, 0);
+        __syncthreads();
+        for (int64_t n0 = n_lo; n0 < n_hi; n0 += 2 * BN) {  // the last stage may be one of zeros
+            step(n0, 0, g1, g0);
+            step(n0 + BN, 1, g0, g1);
         }
     }
     const int64_t tiles = (a.K + 127) / 128;
-    char* const out = a.out + blockIdx.z * a.part_stride;
+    char* const out = a.out + part * a.part_stride;
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
@@ -162,11 +183,12 @@ __global__ __launch_bounds__(256) void add_parts_kernel(const float* __restrict_
 
 }  // namespace
 
-// Parts that the tokens are split into: as many as still give the chip no more than two rounds of tiles, and at
-// least 256 tokens a part.
+// Parts that the tokens are split into: as many as keep the workgroups within one a compute unit of 256, and at least
+// 256 tokens a part (768 x 768 over 6304 tokens, 36 tiles: 27.9 us with 7 parts, 30.8 with 14; 1024 x 4096 over 2048 tokens,
+// 256 tiles: 37.7 in one part, 41.2 in two; 2048 x 1024 over 300 tokens: 15.6 in one part, 22.5 in two).
 int grad_weight_parts(int64_t M, int64_t K, int64_t N) {
     const int64_t tiles = ((M + BT - 1) / BT) * ((K + BT - 1) / BT);
-    const int64_t want = 512 / tiles, most = N / 256;
+    const int64_t want = 256 / tiles, most = N / 256;
     const int64_t p = want < most ? want : most;
     return (int)(p < 1 ? 1 : p);
 }
@@ -178,8 +200,10 @@ hipError_t launch_grad_weight(const Fp8GradArgs& g, hipStream_t s) {
     a.dY = static_cast<const char*>(g.dY); a.X = g.X; a.xs = g.xs;
     a.N = g.N; a.M = g.M; a.K = g.K; a.lddy = g.lddy; a.ldx = g.ldx; a.lds = g.lds;
     const int64_t per = (g.N + parts - 1) / parts;
-    a.per = (per + BN - 1) / BN * BN;
-    const dim3 grid((unsigned)((g.K + BT - 1) / BT), (unsigned)((g.M + BT - 1) / BT), (unsigned)parts);
+    a.per = (per + 2 * BN - 1) / (2 * BN) * (2 * BN);
+    a.tilesK = (int)((g.K + BT - 1) / BT);
+    a.tiles = a.tilesK * (int)((g.M + BT - 1) / BT);
+    const dim3 grid((unsigned)(a.tiles * parts));
     if (parts == 1) {
         a.meta = g.meta; a.out = static_cast<char*>(g.dW); a.ldw = g.ldw; a.part_stride = 0;
         if (g.out_fp32) hipLaunchKernelGGL((grad_weight_kernel<true>), grid, dim3(256), 0, s, a);
