@@ -16,7 +16,7 @@
 namespace sp24 {
 namespace {
 
-constexpr int BT = 256, BN = 64, WT = 128, F = WT / 16;
+constexpr int BT = 256, BN = 64, WK = 128, WM = 64, FK = WK / 16, FM = WM / 16;
 constexpr int HALF_BYTES = BN * BT * 2, STAGE_BYTES = 2 * HALF_BYTES;  // x, then dY
 constexpr uint32_t OOR = 0x80000000u;
 constexpr int GROUP = 8;
@@ -61,14 +61,14 @@ __device__ __forceinline__ bf16x8 frag(uint32_t p) {
     return __builtin_bit_cast(bf16x8, i16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 }
 
-// A thread's codes of a stage: unit (16 codes) t % 16 of tokens t / 16 + 16 h, and their scales.
+// A thread's codes of a stage: unit (16 codes) t % 16 of tokens t / 16 + 32 h, and their scales.
 struct Codes {
-    u32x4 x[4];
-    uint32_t s[4];
+    u32x4 x[2];
+    uint32_t s[2];
 };
 
 template <bool F32>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void grad_weight_tiled_kernel(Args a) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void grad_weight_tiled_kernel(Args a) {
     __shared__ __attribute__((aligned(128))) char smem[2 * STAGE_BYTES];
     const uint32_t l0 = (uint32_t)(size_t)(lds_char*)smem;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, q = lane >> 4;
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int gsize = GROUP * a.tilesK, grp = L / gsize, first = grp * GROUP;
     const int gm = (a.tilesM - first) < GROUP ? (a.tilesM - first) : GROUP, in_g = L - grp * gsize;
     const int64_t m0 = (int64_t)(first + in_g % gm) * BT, k0 = (int64_t)(in_g / gm) * BT;
-    const int wk = (wave >> 1) * WT, wm = (wave & 1) * WT;
+    const int wk = (wave >> 2) * WK, wm = (wave & 3) * WM;
     const int S = (int)((a.N + BN - 1) / BN);
 
     // codes: offsets from the stage's first token; units past K are out of range, tokens past N past the extent
@@ -99,28 +99,28 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
                           rsrc(a.xs + n * a.lds + (k0 >> 7), s < S ? (a.N - 1 - n) * a.lds + (a.K + 127) / 128 - (k0 >> 7) : 0)};
     };
     auto load_codes = [&](const CodeSource& src, int h, Codes& c) {
-        c.x[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(src.x, (int)(xo + (xk ? 16u * h * (uint32_t)a.ldx : 0u)), 0, 0));
-        c.s[h] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(src.s, (int)(so + (xk ? 16u * h * (uint32_t)a.lds : 0u)), 0, 0);
+        c.x[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(src.x, (int)(xo + (xk ? 32u * h * (uint32_t)a.ldx : 0u)), 0, 0));
+        c.s[h] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(src.s, (int)(so + (xk ? 32u * h * (uint32_t)a.lds : 0u)), 0, 0);
     };
-    // dY: load h of a wave fills tokens 16 wave + 2 h, + 1; lane i the 16 bytes i % 32 of token i / 32, which belong to
+    // dY: load h of a wave fills tokens 8 wave + 2 h, + 1; lane i the 16 bytes i % 32 of token i / 32, which belong to
     // unit (i % 32) / 2 ^ swz
-    uint32_t yo[4];  // by h & 1 and h / 4: swz of tokens 2 h, 2 h + 1 depends on no more
+    uint32_t yo[2];  // by h & 1: swz of tokens 2 h, 2 h + 1 depends on no more, but for bit 3, which is the wave's
 #pragma unroll
-    for (int v = 0; v < 4; v++) {
-        const int n = 2 * (v & 1) + 8 * (v >> 1) + (lane >> 5), u = ((lane & 31) >> 1) ^ swz(n);
+    for (int v = 0; v < 2; v++) {
+        const int n = 8 * wave + 2 * v + (lane >> 5), u = ((lane & 31) >> 1) ^ swz(n);
         yo[v] = (uint32_t)(((lane >> 5) * (int)a.lddy + 16 * u + 8 * (lane & 1)) * 2);
     }
     auto dy_source = [&](int s) {
-        const int64_t n = (int64_t)s * BN + 16 * wave;
+        const int64_t n = (int64_t)s * BN + 8 * wave;
         const int64_t bytes = ((a.N - 1 - n) * a.lddy + a.M - m0) * 2;
         return make_rsrc(a.dY + (n * a.lddy + m0) * 2, s < S ? (bytes + 3) & ~(int64_t)3 : 0);
     };
     auto load_dy = [&](const i32x4& src, int h, uint32_t buf) {
-        dma16(buf + HALF_BYTES + (16 * wave + 2 * h) * 512, yo[(h & 1) + 2 * (h >> 2)] + (uint32_t)(2 * h * (int)a.lddy * 2), src);
+        dma16(buf + HALF_BYTES + (8 * wave + 2 * h) * 512, yo[h & 1] + (uint32_t)(2 * h * (int)a.lddy * 2), src);
     };
     // half e (8 codes) of unit h, as bf16
     auto write_codes = [&](const Codes& c, int h, int e, uint32_t buf) {
-        const int n = xt + 16 * h;
+        const int n = xt + 32 * h;
         const float s = scale_value(c.s[h]);
         u32x4 w;
 #pragma unroll
@@ -135,79 +135,82 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int row = 8 * q + (r >> 2), rs = swz(row);
     const uint32_t po = (uint32_t)(row * 512 + 8 * (r & 3));
     auto place = [&](int c) { return po + (uint32_t)(((c >> 4) ^ rs) << 5); };
-    uint32_t px[F], py[F];  // c >> 4 runs over 8 units: c = wk + 16 i
+    uint32_t px[FK], py[FM];
 #pragma unroll
-    for (int i = 0; i < F; i++) px[i] = place(wk + 16 * i), py[i] = HALF_BYTES + place(wm + 16 * i);
+    for (int i = 0; i < FK; i++) px[i] = place(wk + 16 * i);
+#pragma unroll
+    for (int j = 0; j < FM; j++) py[j] = HALF_BYTES + place(wm + 16 * j);
 
-    f32x4 acc[F][F];
+    f32x4 acc[FK][FM];
 #pragma unroll
-    for (int i = 0; i < F; i++)
+    for (int i = 0; i < FK; i++)
 #pragma unroll
-        for (int j = 0; j < F; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < FM; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     Codes c, next;
     {
         const CodeSource c0 = code_source(0), c1 = code_source(1), c2 = code_source(2);
         const i32x4 d0 = dy_source(0), d1 = dy_source(1);
 #pragma unroll
-        for (int h = 0; h < 4; h++) load_codes(c0, h, c);
+        for (int h = 0; h < 2; h++) load_codes(c0, h, c);
 #pragma unroll
-        for (int h = 0; h < 8; h++) load_dy(d0, h, l0);
+        for (int h = 0; h < 4; h++) load_dy(d0, h, l0);
 #pragma unroll
-        for (int h = 0; h < 4; h++) load_codes(c1, h, next);
+        for (int h = 0; h < 2; h++) load_codes(c1, h, next);
         __builtin_amdgcn_s_waitcnt(0x0F70);
 #pragma unroll
-        for (int h = 0; h < 4; h++) write_codes(c, h, 0, l0), write_codes(c, h, 1, l0);
+        for (int h = 0; h < 2; h++) write_codes(c, h, 0, l0), write_codes(c, h, 1, l0);
         c = next;
 #pragma unroll
-        for (int h = 0; h < 8; h++) load_dy(d1, h, l0 + STAGE_BYTES);
+        for (int h = 0; h < 4; h++) load_dy(d1, h, l0 + STAGE_BYTES);
 #pragma unroll
-        for (int h = 0; h < 4; h++) load_codes(c2, h, next);
+        for (int h = 0; h < 2; h++) load_codes(c2, h, next);
     }
     __syncthreads();
 
-    bf16x8 x[F], y0[F], y1[F];  // an x fragment is replaced by the next step's after its row of products
+    bf16x8 x[FK], y0[FM], y1[FM];  // an x fragment is replaced by the next step's after its row of products
 #pragma unroll
-    for (int i = 0; i < F; i++) x[i] = frag(l0 + px[i]), y0[i] = frag(l0 + py[i]);
+    for (int i = 0; i < FK; i++) x[i] = frag(l0 + px[i]);
+#pragma unroll
+    for (int j = 0; j < FM; j++) y0[j] = frag(l0 + py[j]);
 
     uint32_t cur = l0, oth = l0 + STAGE_BYTES;
 #pragma unroll 1
     for (int s = 0; s < S; s++) {
-        // step 0, with the fragments of step 1 and the codes of the next stage. The matrix unit is busy for four issue
-        // slots of an instruction, so a wave alone on its SIMD keeps it fed only if no more than three others stand
-        // between two of them: the side work is dealt out in such pieces.
+        // step 0, with the fragments of step 1 and the codes of the next stage: side work behind single matrix
+        // instructions, so that it runs beside them
 #pragma unroll
-        for (int i = 0; i < F; i++)
+        for (int i = 0; i < FK; i++)
 #pragma unroll
-            for (int j = 0; j < F; j++) {
+            for (int j = 0; j < FM; j++) {
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y0[j], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
-                if (j == 0) y1[i] = frag(cur + py[i] + 32 * 512);
+                if (j == 0 && i < FM) y1[i] = frag(cur + py[i] + 32 * 512);
                 if (j == 2 && i > 0) x[i - 1] = frag(cur + px[i - 1] + 32 * 512);
-                if (j == 4) write_codes(c, i >> 1, i & 1, oth);
+                if (j == 0 && i >= FM) write_codes(c, (i - FM) >> 1, i & 1, oth);
             }
-        x[F - 1] = frag(cur + px[F - 1] + 32 * 512);
+        x[FK - 1] = frag(cur + px[FK - 1] + 32 * 512);
         __builtin_amdgcn_s_waitcnt(0x0070);  // every load and LDS access of this wave is done
         __builtin_amdgcn_s_barrier();
         // step 1, with the fragments of the next stage's step 0 and the loads of stages s + 2 (dY) and s + 3 (codes)
         const i32x4 dsrc = dy_source(s + 2);
         const CodeSource csrc = code_source(s + 3);
 #pragma unroll
-        for (int i = 0; i < F; i++)
+        for (int i = 0; i < FK; i++)
 #pragma unroll
-            for (int j = 0; j < F; j++) {
+            for (int j = 0; j < FM; j++) {
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y1[j], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
-                if (j == 0) y0[i] = frag(oth + py[i]);
+                if (j == 0 && i < FM) y0[i] = frag(oth + py[i]);
                 if (j == 2 && i > 0) x[i - 1] = frag(oth + px[i - 1]);
-                if (j == 4) load_dy(dsrc, i, cur);
-                if (j == 6 && i < 4) {
-                    c.x[i] = next.x[i];
-                    c.s[i] = next.s[i];
-                    load_codes(csrc, i, next);
+                if (j == 1 && i < 4) load_dy(dsrc, i, cur);
+                if (j == 0 && i >= FM && i < FM + 2) {
+                    c.x[i - FM] = next.x[i - FM];
+                    c.s[i - FM] = next.s[i - FM];
+                    load_codes(csrc, i - FM, next);
                 }
             }
-        x[F - 1] = frag(oth + px[F - 1]);
+        x[FK - 1] = frag(oth + px[FK - 1]);
         const uint32_t t = cur;
         cur = oth;
         oth = t;
@@ -219,9 +222,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int xl = r & 3, cq = r >> 2;
     constexpr int W = F32 ? 4 : 2, ES = F32 ? 4 : 2;
 #pragma unroll
-    for (int j = 0; j < F; j++)
+    for (int j = 0; j < FM; j++)
 #pragma unroll
-        for (int ig = 0; ig < F / 4; ig++) {
+        for (int ig = 0; ig < FK / 4; ig++) {
             uint32_t v[4][W];
 #pragma unroll
             for (int f = 0; f < 4; f++) {
@@ -259,8 +262,8 @@ hipError_t launch_grad_weight_tiled(const Fp8GradArgs& g, hipStream_t s) {
     a.tilesK = (int)((g.K + BT - 1) / BT);
     a.tilesM = (int)((g.M + BT - 1) / BT);
     const dim3 grid((unsigned)((int64_t)a.tilesK * a.tilesM));
-    if (g.out_fp32) hipLaunchKernelGGL((grad_weight_tiled_kernel<true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grad_weight_tiled_kernel<false>), grid, dim3(256), 0, s, a);
+    if (g.out_fp32) hipLaunchKernelGGL((grad_weight_tiled_kernel<true>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((grad_weight_tiled_kernel<false>), grid, dim3(512), 0, s, a);
     return hipGetLastError();
 }
 
