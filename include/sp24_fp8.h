@@ -18,8 +18,9 @@
  * Conventions are those of sp24.h (caller-owned device memory, asynchronous on `stream`, validated on the host
  * before any launch, K a positive multiple of 16, M, N >= 1). In addition: base pointers of matrices are 16-byte
  * aligned; a pitch in bytes is a multiple of 16, except that of an output Y (any pitch) and of scales; pitches are
- * below 2^24 elements, K is at most 2^20, and N and M are below 2^31. Results are deterministic: no sum depends
- * on the order in which workgroups run.
+ * below 2^23 elements, those of scales below 2^22; K is at most 2^20, N below 2^31, M at most 2^22 (a launch that
+ * would need 2^24 workgroups or more is SP24_ERR_SHAPE). Results are deterministic: no sum depends on the order in
+ * which workgroups run.
  */
 #ifndef SP24_FP8_H
 #define SP24_FP8_H
@@ -74,7 +75,10 @@ int sp24_decompress_fp8(const uint8_t* values, const uint8_t* meta, const uint8_
  *   infinity). X codes: N x K, pitch ldx. Inside a block the 8-bit matrix instructions align the 64 products to about
  *   2^-13 of the largest one (measured), far below the codes' own 2^-4 and invisible after rounding to 16 bits; an
  *   FP32 result would promise more than that, so none is offered.
- * A NaN scale of x makes its token's row NaN. The product of two scales must be below 2^128. */
+ * A NaN scale of x makes its token's row NaN. The product of two scales must be below 2^128. With many tokens a block
+ * whose product of scales is less than 2^-64 of the largest one before it in its sum is left out (what it would add is
+ * below 2^-40 of that larger unit); for blocks within 2^64 of each other results depend on the sizes, which choose the
+ * kernel, only through the order of the fp32 sums. */
 int sp24_gemm_fp8(const uint8_t* values, const uint8_t* meta, const uint8_t* w_scales, int64_t M, int64_t K,
                   const uint8_t* X, int64_t N, int64_t ldx, const uint8_t* x_scales, int64_t lds, void* Y, int out_dtype,
                   int64_t ldy, void* stream);

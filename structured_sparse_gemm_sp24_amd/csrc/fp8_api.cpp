@@ -10,11 +10,12 @@
 
 namespace {
 
-constexpr int64_t kMaxPitch = (int64_t)1 << 24;  // elements
+constexpr int64_t kMaxPitch = (int64_t)1 << 23;   // elements: 64 rows of any type stay within 32-bit byte offsets
+constexpr int64_t kMaxScalePitch = (int64_t)1 << 22;  // 256 rows likewise
 constexpr int64_t kMaxK = (int64_t)1 << 20, kMaxNormK = 32768;
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxWeightRows = (int64_t)1 << 22;
-constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads in one launch
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool is_float(int dt) { return dt == SP24_BF16 || dt == SP24_FP16 || dt == SP24_FP32; }
@@ -29,7 +30,7 @@ int check_matrix(const void* p, int64_t cols, int64_t ld, int es) {
     if (ld < cols || ld >= kMaxPitch) return SP24_ERR_SHAPE;
     return aligned16(p) && (ld * es) % 16 == 0 ? SP24_OK : SP24_ERR_ALIGN;
 }
-int check_scales(int64_t K, int64_t lds) { return lds < blocks_of(K) || lds >= kMaxPitch ? SP24_ERR_SHAPE : SP24_OK; }
+int check_scales(int64_t K, int64_t lds) { return lds < blocks_of(K) || lds >= kMaxScalePitch ? SP24_ERR_SHAPE : SP24_OK; }
 
 int hip_status(hipError_t e) { return e == hipSuccess ? SP24_OK : SP24_ERR_HIP; }
 
@@ -51,7 +52,6 @@ int sp24_quant_fp8(const void* X, int dtype, int64_t N, int64_t K, int64_t ldx, 
     SP24_TRY(check_matrix(X, K, ldx, type_size(dtype)));
     SP24_TRY(check_matrix(codes, K, ldc, 1));
     SP24_TRY(check_scales(K, lds));
-    if (N > kMaxGrid / (blocks_of(K) * 16) * 256) return SP24_ERR_SHAPE;  // one thread for 8 elements
     SP24_TRY(sp24::check_device());
     return hip_status(sp24::launch_quant_fp8(X, dtype, N, K, ldx, codes, ldc, scales, lds, static_cast<hipStream_t>(stream)));
 }
@@ -111,7 +111,7 @@ int sp24_prune_compress_fp8(const void* W, int dtype, int64_t M, int64_t K, int6
     if (score == SP24_SCORE_WANDA && !norms) return SP24_ERR_NULL;
     if (score == SP24_SCORE_MAGNITUDE && norms) return SP24_ERR_ARG;
     SP24_TRY(check_nk(M, K, kMaxK));
-    if (M > kMaxWeightRows) return SP24_ERR_SHAPE;
+    if (M > kMaxWeightRows || blocks_of(M) * blocks_of(K) > kMaxGrid) return SP24_ERR_SHAPE;
     SP24_TRY(check_matrix(W, K, ldw, type_size(dtype)));
     if (!aligned16(values) || !aligned16(meta) || (norms && !aligned16(norms))) return SP24_ERR_ALIGN;
     SP24_TRY(sp24::check_device());
@@ -124,7 +124,7 @@ int sp24_decompress_fp8(const uint8_t* values, const uint8_t* meta, const uint8_
     if (!values || !meta || !w_scales || !W_out) return SP24_ERR_NULL;
     if (out_dtype != SP24_BF16 && out_dtype != SP24_FP32) return SP24_ERR_DTYPE;
     SP24_TRY(check_nk(M, K, kMaxK));
-    if (M > kMaxWeightRows) return SP24_ERR_SHAPE;
+    if (M > kMaxWeightRows || (M + 15) / 16 * ((blocks_of(K) + 3) / 4) > kMaxGrid) return SP24_ERR_SHAPE;
     SP24_TRY(check_matrix(W_out, K, ldw, type_size(out_dtype)));
     if (!aligned16(values) || !aligned16(meta)) return SP24_ERR_ALIGN;
     SP24_TRY(sp24::check_device());
@@ -138,7 +138,8 @@ int sp24_gemm_fp8(const uint8_t* values, const uint8_t* meta, const uint8_t* w_s
     if (!values || !meta || !w_scales || !X || !x_scales || !Y) return SP24_ERR_NULL;
     if (out_dtype != SP24_BF16 && out_dtype != SP24_FP16) return SP24_ERR_DTYPE;
     SP24_TRY(check_nk(N, K, kMaxK));
-    if (M < 1 || M > kMaxWeightRows) return SP24_ERR_SHAPE;
+    // tiles of 256 x 128: one workgroup each where K is a single block
+    if (M < 1 || M > kMaxWeightRows || ((M + 255) / 256) * blocks_of(N) > kMaxGrid) return SP24_ERR_SHAPE;
     SP24_TRY(check_matrix(X, K, ldx, 1));
     SP24_TRY(check_scales(K, lds));
     if (ldy < M || ldy >= kMaxPitch) return SP24_ERR_SHAPE;

@@ -241,15 +241,28 @@ __global__ __launch_bounds__(1024) void dgamma_kernel(const float* __restrict__ 
 
 constexpr int WPB = 8;  // waves of a workgroup of the gradient kernel where a row is one wave's
 
+constexpr int64_t kRows = (int64_t)1 << 20;  // rows of one launch: below 2^32 threads at any width
+
 template <int DT, int TPR, int C>
-hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+hipError_t launch_norm(NormArgs a, hipStream_t s) {
+    constexpr int B = type_bytes<DT>();
     const unsigned rpb = TPR == 64 ? 4 : 1, threads = TPR == 64 ? 256 : TPR;
-    const dim3 grid((unsigned)((a.N + rpb - 1) / rpb));
-    if (a.R)
-        hipLaunchKernelGGL((rmsnorm_kernel<DT, TPR, C, true>), grid, dim3(threads), 0, s, a);
-    else
-        hipLaunchKernelGGL((rmsnorm_kernel<DT, TPR, C, false>), grid, dim3(threads), 0, s, a);
-    return hipGetLastError();
+    for (int64_t left = a.N; left > 0; left -= kRows) {
+        a.N = left < kRows ? left : kRows;
+        const dim3 grid((unsigned)((a.N + rpb - 1) / rpb));
+        if (a.R)
+            hipLaunchKernelGGL((rmsnorm_kernel<DT, TPR, C, true>), grid, dim3(threads), 0, s, a);
+        else
+            hipLaunchKernelGGL((rmsnorm_kernel<DT, TPR, C, false>), grid, dim3(threads), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.X += kRows * a.ldx * B;
+        if (a.R) a.R += kRows * a.ldr * B, a.H += kRows * a.ldh * B;
+        a.codes += kRows * a.ldc;
+        a.scales += kRows * a.lds;
+        if (a.rstd) a.rstd += kRows;
+    }
+    return hipSuccess;
 }
 
 // Threads of a row and chunks of a thread by the row's length.
@@ -288,11 +301,18 @@ hipError_t launch_back_k(const BackArgs& a, int grid, hipStream_t s) {
 template <int DT>
 hipError_t launch_quant(const void* X, int64_t N, int64_t K, int64_t ldx, uint8_t* codes, int64_t ldc, uint8_t* scales,
                         int64_t lds, hipStream_t s) {
-    const uint32_t per_row = (uint32_t)((K + 127) / 128 * 16);
-    const uint64_t blocks = ((uint64_t)N * per_row + 255) / 256;
-    hipLaunchKernelGGL((quant_kernel<DT>), dim3((unsigned)blocks), dim3(256), 0, s, static_cast<const char*>(X), N, K,
-                       ldx, per_row, codes, ldc, scales, lds);
-    return hipGetLastError();
+    const uint32_t per_row = (uint32_t)((K + 127) / 128 * 16);  // at most 2^17
+    const int64_t most = ((int64_t)1 << 31) / per_row;          // rows of one launch
+    for (int64_t n = 0; n < N; n += most) {
+        const int64_t rows = N - n < most ? N - n : most;
+        const uint64_t blocks = ((uint64_t)rows * per_row + 255) / 256;
+        hipLaunchKernelGGL((quant_kernel<DT>), dim3((unsigned)blocks), dim3(256), 0, s,
+                           static_cast<const char*>(X) + n * ldx * type_bytes<DT>(), rows, K, ldx, per_row, codes + n * ldc,
+                           ldc, scales + n * lds, lds);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

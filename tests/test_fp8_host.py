@@ -31,8 +31,8 @@ QUANT = dict(X=A, dtype=BF16, N=2, K=48, ldx=48, codes=B, ldc=48, scales=C, lds=
     (dict(X=None), NULL), (dict(codes=None), NULL), (dict(scales=None), NULL), (dict(dtype=I8), DTYPE),
     (dict(dtype=FP8), DTYPE), (dict(dtype=-1), DTYPE), (dict(N=0), SHAPE), (dict(K=0), SHAPE), (dict(K=40), SHAPE), (dict(ldx=32), SHAPE),
     (dict(ldc=32), SHAPE), (dict(lds=0), SHAPE), (dict(K=144, ldx=144, ldc=144, lds=1), SHAPE),
-    (dict(K=1 << 21, ldx=1 << 21, ldc=1 << 21, lds=1 << 14), SHAPE), (dict(ldx=1 << 24), SHAPE), (dict(N=1 << 31), SHAPE),
-    (dict(N=(1 << 31) - 1, K=1 << 20, ldx=1 << 20, ldc=1 << 20, lds=1 << 13), SHAPE),  # more workgroups than a grid has
+    (dict(K=1 << 21, ldx=1 << 21, ldc=1 << 21, lds=1 << 14), SHAPE), (dict(ldx=1 << 23), SHAPE), (dict(lds=1 << 22), SHAPE),
+    (dict(N=1 << 31), SHAPE),
     (dict(X=MIS), ALIGN), (dict(codes=MIS), ALIGN), (dict(ldx=52), ALIGN), (dict(ldc=56), ALIGN),
 ])
 def test_quant_validation(lib, bad, expect):  # noqa: F811
@@ -78,6 +78,7 @@ PRUNE = dict(W=A, dtype=BF16, M=4, K=48, ldw=48, score=0, norms=None, values=B, 
     (dict(score=1), NULL), (dict(norms=A), ARG), (dict(score=2), ARG), (dict(dtype=I8), DTYPE), (dict(M=0), SHAPE),
     (dict(K=24), SHAPE), (dict(ldw=32), SHAPE), (dict(W=MIS), ALIGN), (dict(values=MIS), ALIGN), (dict(meta=MIS), ALIGN),
     (dict(score=1, norms=MIS), ALIGN), (dict(ldw=52), ALIGN), (dict(M=(1 << 22) + 1), SHAPE),
+    (dict(M=1 << 22, K=1 << 20, ldw=1 << 20), SHAPE),
 ])
 def test_prune_compress_fp8_validation(lib, bad, expect):  # noqa: F811
     assert lib.sp24_prune_compress_fp8(*changed(PRUNE, **bad)) == expect
@@ -102,7 +103,7 @@ GEMM = dict(values=A, meta=B, w_scales=C, M=4, K=48, X=D, N=2, ldx=48, x_scales=
     (dict(x_scales=None), NULL), (dict(Y=None), NULL), (dict(out_dtype=FP32), DTYPE), (dict(out_dtype=FP8), DTYPE),
     (dict(M=0), SHAPE), (dict(N=0), SHAPE), (dict(K=40), SHAPE), (dict(ldx=32), SHAPE), (dict(lds=0), SHAPE), (dict(ldy=3), SHAPE),
     (dict(X=MIS), ALIGN), (dict(Y=MIS), ALIGN), (dict(values=MIS), ALIGN), (dict(meta=MIS), ALIGN), (dict(ldx=56), ALIGN),
-    (dict(M=(1 << 22) + 1, ldy=(1 << 22) + 1), SHAPE),
+    (dict(M=(1 << 22) + 1, ldy=(1 << 22) + 1), SHAPE), (dict(M=1 << 22, ldy=1 << 22, N=1 << 30), SHAPE),
 ])
 def test_gemm_fp8_validation(lib, bad, expect):  # noqa: F811
     assert lib.sp24_gemm_fp8(*changed(GEMM, **bad)) == expect

@@ -281,7 +281,8 @@ def test_prune_compress_zero_and_tiny_blocks():
 GEMM_SIZES = [(1, 16, 1), (16, 128, 1), (17, 144, 2), (130, 272, 3), (257, 128, 16), (300, 1040, 17), (64, 4096, 33),
               (515, 1024, 37), (1100, 272, 64), (129, 2064, 65), (256, 128, 128), (256, 256, 129), (1000, 1152, 200),
               (2050, 400, 300), (4100, 4096, 5), (9000, 256, 40), (18000, 128, 20), (600, 512, 1000), (4096, 640, 513),
-              (4100, 272, 4090), (4096, 384, 4096), (8200, 112, 2050)]
+              (4100, 272, 4090), (4096, 384, 4096), (8200, 112, 2050), (4100, 144, 1000), (9000, 384, 300), (4100, 128, 900),
+              (8200, 256, 4100)]
 
 
 def int_case(M, K, N, seed=0):
