@@ -1,7 +1,9 @@
 """Build libsp24.so (the C-ABI library with its HIP kernels) for gfx950, in-tree.
 
 Each source compiles to an object under <repo>/_build with hipcc (in parallel), then one hipcc link
-produces structured_sparse_gemm_sp24_amd/libsp24.so. hipcc cross-compiles, so no GPU is needed.
+produces structured_sparse_gemm_sp24_amd/libsp24.so. hipcc cross-compiles, so no GPU is needed. The native
+marshalling of the 8-bit operators (binding/fp8_binding.cpp) compiles with g++ against torch's headers into the
+extension module _fp8_binding.so, which links to libsp24.so beside it.
 """
 from __future__ import annotations
 
@@ -9,12 +11,15 @@ import concurrent.futures
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsp24.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
+BINDING_SRC = os.path.join(PKG, "binding", "fp8_binding.cpp")
+BINDING = os.path.join(PKG, "_fp8_binding.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -37,20 +42,50 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_binding(_=None) -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD_DIR, "fp8_binding.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-lsp24", "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-ltorch_hip", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     workers = max(1, min(len(srcs), int(os.environ.get("MAX_JOBS", "8"))))
     with concurrent.futures.ThreadPoolExecutor(workers) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libsp24.so", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {BINDING}")
     return LIB
 
 
