@@ -111,7 +111,7 @@ int sp24_prune_compress_fp8(const void* W, int dtype, int64_t M, int64_t K, int6
     if (score == SP24_SCORE_WANDA && !norms) return SP24_ERR_NULL;
     if (score == SP24_SCORE_MAGNITUDE && norms) return SP24_ERR_ARG;
     SP24_TRY(check_nk(M, K, kMaxK));
-    if (M > kMaxWeightRows || blocks_of(M) * blocks_of(K) > kMaxGrid) return SP24_ERR_SHAPE;
+    if (M > kMaxWeightRows || blocks_of(M) * blocks_of(K) > kMaxGrid / 2) return SP24_ERR_SHAPE;  // 512 threads
     SP24_TRY(check_matrix(W, K, ldw, type_size(dtype)));
     if (!aligned16(values) || !aligned16(meta) || (norms && !aligned16(norms))) return SP24_ERR_ALIGN;
     SP24_TRY(sp24::check_device());

@@ -511,56 +511,56 @@ hipError_t launch_decompress(const void* values, const uint8_t* meta, int dtype,
 
 
 // Prune + compress to e4m3 values with one power-of-two scale for each 128 x 128 block of the weight. A workgroup
-// owns one block: eight 16-row tiles of 128 columns, wave w tiles w and w + 4, lane l of a tile row l % 16 and
-// columns [32 (l / 16), +32) as above. It selects in registers, takes the largest kept magnitude over the
-// workgroup, and writes the kept values times 2^(127 - scale), rounded once.
+// owns one block: eight 16-row tiles of 128 columns, one a wave, lane l of a tile row l % 16 and columns
+// [32 (l / 16), +32) as above. It selects in registers, takes the largest kept magnitude over the workgroup, and
+// writes the kept values times 2^(127 - scale), rounded once.
+//
+// HBM bounds it: 28672 x 8192 in 140 us from bf16 (4.4 TB/s) and 236 from fp32 (4.6). A lane's span is 64 or 128 bytes, read
+// by several loads, so these keep the caches' default: with the non-temporal hint the lines came from HBM again for
+// each load (207 and 716 us). Two tiles a wave took 139 and 272 us.
 template <int DT, bool WANDA>
-__global__ __launch_bounds__(256) void prune_compress_fp8_kernel(const char* __restrict__ W, int64_t ldw, int64_t M,
+__global__ __launch_bounds__(512) void prune_compress_fp8_kernel(const char* __restrict__ W, int64_t ldw, int64_t M,
                                                                  int64_t K, uint32_t tiles,
                                                                  const float* __restrict__ norms,
                                                                  uint8_t* __restrict__ values, uint8_t* __restrict__ meta,
                                                                  uint8_t* __restrict__ w_scales) {
     constexpr int isz = esize<DT>(), PER = 16 / isz;
     typedef typename Elem<DT>::T T;
-    __shared__ uint32_t wave_max[4];
+    __shared__ uint32_t wave_max[8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, qq = lane >> 4;
     const uint32_t mb = blockIdx.x / tiles, t = blockIdx.x - mb * tiles;
     const int64_t c0 = (int64_t)t * 128 + 32 * qq, blocks = (M + 15) / 16;
-    float kept[2][16];
-    uint32_t mbits[2], big = 0;
+    float kept[16];
+    uint32_t mbits = 0, big = 0;
+    const int64_t row = (int64_t)mb * 128 + 16 * wave + r;
+    T x[32];
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int64_t row = (int64_t)mb * 128 + 16 * (wave + 4 * i) + r;
-        T x[32];
+    for (int h = 0; h < 32 / PER; h++) {
+        const int64_t c = c0 + PER * h;
+        u32x4 v = u32x4{0, 0, 0, 0};
+        if (row < M && c < K) v = *reinterpret_cast<const u32x4*>(W + (row * ldw + c) * isz);
 #pragma unroll
-        for (int h = 0; h < 32 / PER; h++) {
-            const int64_t c = c0 + PER * h;
-            u32x4 v = u32x4{0, 0, 0, 0};
-            if (row < M && c < K) v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(W + (row * ldw + c) * isz));
+        for (int e = 0; e < PER; e++)
+            x[PER * h + e] = (T)(isz == 4 ? v[e & 3] : (v[(e >> 1) & 3] >> (16 * (e & 1))) & 0xFFFFu);
+    }
 #pragma unroll
-            for (int e = 0; e < PER; e++)
-                x[PER * h + e] = (T)(isz == 4 ? v[e & 3] : (v[(e >> 1) & 3] >> (16 * (e & 1))) & 0xFFFFu);
+    for (int g = 0; g < 8; g++) {
+        const int64_t c = c0 + 4 * g;
+        int lo = 0, hi = 1;
+        if (row < M && c < K) {
+            uint32_t key[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) key[e] = select_key<DT, WANDA>(x[4 * g + e], WANDA ? norms[c + e] : 0.f);
+            knockout_top2(key, lo, hi);
         }
-        mbits[i] = 0;
+        mbits |= (uint32_t)(lo | (hi << 2)) << (4 * g);
 #pragma unroll
-        for (int g = 0; g < 8; g++) {
-            const int64_t c = c0 + 4 * g;
-            int lo = 0, hi = 1;
-            if (row < M && c < K) {
-                uint32_t key[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++) key[e] = select_key<DT, WANDA>(x[4 * g + e], WANDA ? norms[c + e] : 0.f);
-                knockout_top2(key, lo, hi);
-            }
-            mbits[i] |= (uint32_t)(lo | (hi << 2)) << (4 * g);
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const T v = pick4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3], e ? hi : lo);
-                kept[i][2 * g + e] = DT == DT_FP32 ? __uint_as_float((uint32_t)v)
-                                                   : (DT == DT_FP16 ? f16_to_f32((uint16_t)v) : bf16_to_f32((uint16_t)v));
-                const uint32_t a = __float_as_uint(kept[i][2 * g + e]) & 0x7FFFFFFFu;
-                big = a > big ? a : big;
-            }
+        for (int e = 0; e < 2; e++) {
+            const T v = pick4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3], e ? hi : lo);
+            kept[2 * g + e] = DT == DT_FP32 ? __uint_as_float((uint32_t)v)
+                                               : (DT == DT_FP16 ? f16_to_f32((uint16_t)v) : bf16_to_f32((uint16_t)v));
+            const uint32_t a = __float_as_uint(kept[2 * g + e]) & 0x7FFFFFFFu;
+            big = a > big ? a : big;
         }
     }
     big = max16(big);
@@ -568,51 +568,60 @@ __global__ __launch_bounds__(256) void prune_compress_fp8_kernel(const char* __r
     const uint32_t m23 = max((uint32_t)__builtin_amdgcn_readlane((int)big, 32), (uint32_t)__builtin_amdgcn_readlane((int)big, 48));
     if (lane == 0) wave_max[wave] = max(m01, m23);
     __syncthreads();
-    const uint32_t s = scale_byte(max(max(wave_max[0], wave_max[1]), max(wave_max[2], wave_max[3])));
+    uint32_t m = wave_max[0];
+#pragma unroll
+    for (int w = 1; w < 8; w++) m = max(m, wave_max[w]);
+    const uint32_t s = scale_byte(m);
     const float f = code_factor(s);
     if (threadIdx.x == 0) w_scales[blockIdx.x] = (uint8_t)s;
+    const int64_t b = (int64_t)mb * 8 + wave;
+    if (b >= blocks) return;
+    u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int64_t b = (int64_t)mb * 8 + wave + 4 * i;
-        if (b >= blocks) continue;
-        u32x4 v;
-#pragma unroll
-        for (int w = 0; w < 4; w++)
-            v[w] = codes4(kept[i][4 * w] * f, kept[i][4 * w + 1] * f, kept[i][4 * w + 2] * f, kept[i][4 * w + 3] * f);
-        *reinterpret_cast<u32x4*>(values + (b * tiles + t) * 1024 + 16 * lane) = v;
-        *reinterpret_cast<uint32_t*>(meta + (b * tiles + t) * 256 + 4 * lane) = mbits[i];
-    }
+    for (int w = 0; w < 4; w++) v[w] = codes4(kept[4 * w] * f, kept[4 * w + 1] * f, kept[4 * w + 2] * f, kept[4 * w + 3] * f);
+    *reinterpret_cast<u32x4*>(values + (b * tiles + t) * 1024 + 16 * lane) = v;
+    *reinterpret_cast<uint32_t*>(meta + (b * tiles + t) * 256 + 4 * lane) = mbits;
 }
 
-// The dense weight back from e4m3 values, metadata and scales: one lane per slot of a tile (row l % 16, 32 columns),
-// four tiles of one 16-row block a workgroup.
+// The dense weight back from e4m3 values, metadata and scales: one thread per 16 columns (8 value bytes, 4 groups),
+// numbered in the order of the compressed tiles -- the 16 rows of a row block, then the eight chunks of a tile -- so that
+// a wave reads half a tile in whole 16-byte slots and writes 128 (bf16) or 256 (fp32) consecutive bytes of 16 rows.
+// HBM bounds it: 28672 x 8192 to bf16 131 us, 4.7 TB/s (with a whole slot, 32 columns, a lane: 181 us).
 template <bool F32>
 __global__ __launch_bounds__(256) void decompress_fp8_kernel(const uint8_t* __restrict__ values,
                                                              const uint8_t* __restrict__ meta,
                                                              const uint8_t* __restrict__ w_scales, int64_t M, int64_t K,
                                                              uint32_t tiles, char* __restrict__ W, int64_t ldw) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t per = (tiles + 3) / 4, b = blockIdx.x / per, t = 4 * (blockIdx.x - b * per) + wave;
-    const int64_t row = 16 * (int64_t)b + (lane & 15), c0 = (int64_t)t * 128 + 32 * (lane >> 4);
-    if (t >= tiles || row >= M || c0 >= K) return;
-    const int64_t tile = (int64_t)b * tiles + t;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(values + tile * 1024 + 16 * lane);
-    const uint32_t mb = *reinterpret_cast<const uint32_t*>(meta + tile * 256 + 4 * lane);
-    const float f = scale_value(w_scales[(int64_t)(b >> 3) * tiles + t]);
+    const uint32_t i = threadIdx.x & 127, r = i & 15, c = i >> 4, slot = r + 16 * (c >> 1), h = c & 1;
+    const uint32_t per = (tiles + 3) / 4, b = blockIdx.x / per, t0 = 4 * (blockIdx.x - b * per) + (threadIdx.x >> 7);
+    const int64_t row = 16 * (int64_t)b + r;
+    u32x2 v[2];
+    uint32_t mb[2];
+    float f[2];
+    bool in[2];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {  // 16 columns: K is a multiple of 16
-        if (c0 + 16 * h >= K) break;
+    for (int u = 0; u < 2; u++) {  // four tiles a workgroup
+        const uint32_t t = t0 + 2 * u;
+        in[u] = t < tiles && row < M && (int64_t)t * 128 + 16 * c < K;  // K is a multiple of 16
+        if (!in[u]) continue;
+        const int64_t tile = (int64_t)b * tiles + t;
+        v[u] = *reinterpret_cast<const u32x2*>(values + tile * 1024 + 16 * slot + 8 * h);
+        mb[u] = *reinterpret_cast<const uint16_t*>(meta + tile * 256 + 4 * slot + 2 * h);
+        f[u] = scale_value(w_scales[(int64_t)(b >> 3) * tiles + t]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+        if (!in[u]) continue;
         float o[16];
 #pragma unroll
         for (int g = 0; g < 4; g++) {
-            const int n = 4 * h + g;  // group of the lane's span: value bytes 2n, 2n + 1
-            const uint32_t nib = (mb >> (4 * n)) & 15u;
-            const int word = (int)v[n >> 1];
-            const f32x2 d = (n & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(word, true) : __builtin_amdgcn_cvt_pk_f32_fp8(word, false);
+            const uint32_t nib = (mb[u] >> (4 * g)) & 15u;
+            const int word = (int)v[u][g >> 1];
+            const f32x2 d = (g & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(word, true) : __builtin_amdgcn_cvt_pk_f32_fp8(word, false);
 #pragma unroll
-            for (uint32_t e = 0; e < 4; e++) o[4 * g + e] = e == (nib & 3u) ? d[0] * f : (e == (nib >> 2) ? d[1] * f : 0.f);
+            for (uint32_t e = 0; e < 4; e++) o[4 * g + e] = e == (nib & 3u) ? d[0] * f[u] : (e == (nib >> 2) ? d[1] * f[u] : 0.f);
         }
-        char* const p = W + (row * ldw + c0 + 16 * h) * (F32 ? 4 : 2);
+        char* const p = W + (row * ldw + (int64_t)(t0 + 2 * u) * 128 + 16 * c) * (F32 ? 4 : 2);
 #pragma unroll
         for (int e = 0; e < 2; e++) {
             const float w[8] = {o[8 * e], o[8 * e + 1], o[8 * e + 2], o[8 * e + 3], o[8 * e + 4], o[8 * e + 5], o[8 * e + 6], o[8 * e + 7]};
@@ -628,10 +637,10 @@ static hipError_t launch_pc_fp8(const void* W, int64_t M, int64_t K, int64_t ldw
     const uint32_t tiles = (uint32_t)((K + 127) / 128);
     const dim3 grid((unsigned)((M + 127) / 128 * tiles));
     if (wanda)
-        hipLaunchKernelGGL((prune_compress_fp8_kernel<DT, true>), grid, dim3(256), 0, s, static_cast<const char*>(W), ldw,
+        hipLaunchKernelGGL((prune_compress_fp8_kernel<DT, true>), grid, dim3(512), 0, s, static_cast<const char*>(W), ldw,
                            M, K, tiles, norms, values, meta, w_scales);
     else
-        hipLaunchKernelGGL((prune_compress_fp8_kernel<DT, false>), grid, dim3(256), 0, s, static_cast<const char*>(W), ldw,
+        hipLaunchKernelGGL((prune_compress_fp8_kernel<DT, false>), grid, dim3(512), 0, s, static_cast<const char*>(W), ldw,
                            M, K, tiles, norms, values, meta, w_scales);
     return hipGetLastError();
 }
