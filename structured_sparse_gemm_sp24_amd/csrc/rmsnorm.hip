@@ -30,6 +30,12 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int slot) {
     return s;
 }
 
+// The thread's row among its workgroup's, in a scalar register: addresses then are a scalar base and a 32-bit offset.
+template <int TPR>
+__device__ __forceinline__ int row_of() {
+    return TPR == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+}
+
 // One lane's eight values of a block of 128 (16 lanes) as codes, and the block's scale by its first lane. Lanes past
 // the row's end hold zeros and store nothing.
 __device__ __forceinline__ void store_codes(const float (&y)[8], bool in, uint8_t* codes, uint8_t* scale, int lane) {
@@ -80,7 +86,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rmsnorm_kernel(NormArgs
     __shared__ float red[2][16];
     constexpr int RPB = TPR == 64 ? 4 : 1, B = type_bytes<DT>();
     const int t = threadIdx.x % TPR;
-    const int64_t n = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    const int64_t n = (int64_t)blockIdx.x * RPB + row_of<TPR>();
     if (n >= a.N) return;  // whole waves, and only where no barrier follows (TPR = 64)
     Raw8<DT> x[C], g[C];
     float h[C][8];
@@ -138,48 +144,66 @@ template <int DT, int TPR, int C, int WPB, bool RES>
 __global__ __launch_bounds__(TPR == 64 ? 64 * WPB : TPR) void rmsnorm_back_kernel(BackArgs a) {
     __shared__ float red[2][16];
     constexpr int RPB = TPR == 64 ? WPB : 1, B = type_bytes<DT>();
-    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    Raw8<DT> g[C];
+    // The widest rows leave a thread too few registers (256) to keep a row's numbers unpacked over the reduction, or
+    // dH, or in fp32 gamma: those are read where they are used.
+    constexpr bool TIGHT = C == 8, LATE = TIGHT && DT == T_FP32;
+    const int t = threadIdx.x % TPR, sub = row_of<TPR>();
+    Raw8<DT> g[LATE ? 1 : C];
     float dg[C][8];
 #pragma unroll
     for (int c = 0; c < C; c++) {
         const int k = 8 * (c * TPR + t);
-        g[c] = k < a.K ? load8<DT>(a.gamma + k * B) : zero8<DT>();
+        if constexpr (!LATE) g[c] = k < a.K ? load8<DT>(a.gamma + k * B) : zero8<DT>();
 #pragma unroll
         for (int e = 0; e < 8; e++) dg[c][e] = 0.f;
     }
     int slot = 0;
     for (int64_t n = (int64_t)blockIdx.x * RPB + sub; n < a.N; n += (int64_t)gridDim.x * RPB, slot ^= 1) {
         const float r = a.rstd[n];
-        Raw8<DT> dy[C], h[C], dh[C];
+        Raw8<DT> dy[C], h[C], dh[TIGHT ? 1 : C];
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int k = 8 * (c * TPR + t);
             const bool in = k < a.K;
             dy[c] = in ? load8_once<DT>(a.dY + (n * a.lddy + k) * B) : zero8<DT>();
             h[c] = in ? load8_once<DT>(a.H + (n * a.ldh + k) * B) : zero8<DT>();
-            if constexpr (RES) dh[c] = in ? load8_once<DT>(a.dH + (n * a.lddh + k) * B) : zero8<DT>();
+            if constexpr (RES && !TIGHT) dh[c] = in ? load8_once<DT>(a.dH + (n * a.lddh + k) * B) : zero8<DT>();
         }
         float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < C; c++)
+        for (int c = 0; c < C; c++) {
+            const int k = 8 * (c * TPR + t);
+            if constexpr (LATE) g[0] = k < a.K ? load8<DT>(a.gamma + k * B) : zero8<DT>();
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 const float dyh = elem(dy[c], e) * elem(h[c], e);
-                sum = fmaf(elem(g[c], e), dyh, sum);
+                sum = fmaf(elem(g[LATE ? 0 : c], e), dyh, sum);
                 dg[c][e] = fmaf(dyh, r, dg[c][e]);
             }
+            if constexpr (LATE) __builtin_amdgcn_sched_barrier(0);  // the next chunk's gamma not before this one's
+        }
         const float q = row_sum<TPR>(sum, red, slot) / (float)a.K * r * r;
+        if constexpr (TIGHT)  // unpacked again below
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                asm volatile("" : "+v"(dy[c].w[0]), "+v"(h[c].w[0]));
+                if constexpr (!LATE) asm volatile("" : "+v"(g[c].w[0]));
+            }
 #pragma unroll
         for (int c = 0; c < C; c++) {
-            const int k = 8 * (c * TPR + t);
+            const int k = 8 * (c * TPR + t), i = LATE ? 0 : c, j = TIGHT ? 0 : c;
+            if constexpr (LATE) g[0] = k < a.K ? load8<DT>(a.gamma + k * B) : zero8<DT>();
+            if constexpr (TIGHT && RES) {
+                dh[0] = k < a.K ? load8_once<DT>(a.dH + (n * a.lddh + k) * B) : zero8<DT>();
+            }
             float dx[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                dx[e] = r * fmaf(-elem(h[c], e), q, elem(g[c], e) * elem(dy[c], e));
-                if constexpr (RES) dx[e] += elem(dh[c], e);
+                dx[e] = r * fmaf(-elem(h[c], e), q, elem(g[i], e) * elem(dy[c], e));
+                if constexpr (RES) dx[e] += elem(dh[j], e);
             }
             if (k < a.K) store8<DT>(a.dX + (n * a.lddx + k) * B, pack8<DT>(dx));
+            if constexpr (LATE) __builtin_amdgcn_sched_barrier(0);
         }
     }
     float* const part = a.part + (int64_t)blockIdx.x * a.K;
@@ -265,14 +289,17 @@ hipError_t launch_norm(NormArgs a, hipStream_t s) {
     return hipSuccess;
 }
 
-// Threads of a row and chunks of a thread by the row's length.
+// Threads of a row and chunks of a thread by the row's length (us, bf16 with the residual): many rows run alike
+// (6304 x 768 with 64 threads x 2 chunks 8.9, with 128 x 1 9.1; 8192 x 4096 with 512 x 1 42.3, with 256 x 2 41.6; 8192 x
+// 8192 with 512 x 2 and 256 x 4 76.4; 4096 x 16384 with 1024 x 2 76.8, with 512 x 4 77.4); few are the faster the more
+// threads they have (16 x 4096 2.7 against 2.9, 16 x 8192 3.3 against 3.6).
 template <int DT>
 hipError_t launch_norm_k(const NormArgs& a, hipStream_t s) {
     if (a.K <= 512) return launch_norm<DT, 64, 1>(a, s);
     if (a.K <= 1024) return launch_norm<DT, 64, 2>(a, s);
     if (a.K <= 2048) return launch_norm<DT, 256, 1>(a, s);
-    if (a.K <= 4096) return launch_norm<DT, 256, 2>(a, s);
-    if (a.K <= 8192) return launch_norm<DT, 256, 4>(a, s);
+    if (a.K <= 4096) return launch_norm<DT, 512, 1>(a, s);
+    if (a.K <= 8192) return launch_norm<DT, 512, 2>(a, s);
     if (a.K <= 16384) return launch_norm<DT, 1024, 2>(a, s);
     return launch_norm<DT, 1024, 4>(a, s);
 }
@@ -287,6 +314,9 @@ hipError_t launch_back(const BackArgs& a, int grid, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The same for the gradients: 8192 x 2048 with 256 threads x 1 chunk 30.3 us, with 64 x 4 32.4; 8192 x 8192 with 256 x 4 92.0,
+// with 512 x 2 93.7; 4096 x 16384 with 1024 x 2 98, with 512 x 4 99.5; 4096 x 32768 with 512 x 8 220, with 1024 x 4 (whose 128
+// registers a thread spill) 632.
 template <int DT>
 hipError_t launch_back_k(const BackArgs& a, int grid, hipStream_t s) {
     if (a.K <= 512) return launch_back<DT, 64, 1>(a, grid, s);
@@ -295,7 +325,7 @@ hipError_t launch_back_k(const BackArgs& a, int grid, hipStream_t s) {
     if (a.K <= 4096) return launch_back<DT, 256, 2>(a, grid, s);
     if (a.K <= 8192) return launch_back<DT, 256, 4>(a, grid, s);
     if (a.K <= 16384) return launch_back<DT, 1024, 2>(a, grid, s);
-    return launch_back<DT, 1024, 4>(a, grid, s);
+    return launch_back<DT, 512, 8>(a, grid, s);
 }
 
 template <int DT>
@@ -340,10 +370,12 @@ hipError_t launch_rmsnorm(const void* X, int dtype, int64_t N, int64_t K, int64_
     }
 }
 
-// Workgroups (and rows of partial sums) of the gradient kernel.
+// Workgroups (and rows of partial sums) of the gradient kernel: more of them hide more latency, fewer leave fewer partial
+// sums (us with 256 / 512 / 1024: 65536 x 768 70.5 / 74.6 / 74.3, 8192 x 4096 57.9 / 50.5 / 55.1, 8192 x 8192 100.8 / 91.1 /
+// 97.9, 4096 x 16384 96.5 / 102.5 / 113.8).
 int rmsnorm_back_parts(int64_t N, int64_t K) {
     const int64_t rows = K <= 1024 ? (N + WPB - 1) / WPB : N;
-    const int64_t most = K <= 1024 ? 512 : (K <= 8192 ? 512 : 256);
+    const int64_t most = K <= 1024 || K > 8192 ? 256 : 512;
     return (int)(rows < most ? rows : most);
 }
 
