@@ -507,9 +507,17 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
 
 }  // namespace
 
+// Tile width by the rounds of the chip that the tiles take: one 256-wide tile a compute unit, or two 128-wide ones. A round
+// of 256-wide tiles is the faster where it is full enough that the 128-wide tiles (half as many columns each) would
+// need their last round's second half as well, and always from four rounds on. Measured (us, 128 wide / 256 wide;
+// tiles of 256 x 256): 11008 x 4096 at N = 512 (86) 37.7 / 51.3, 700 (129) 57.9 / 56.2, 1024 (172) 62.2 / 56.3, 1500 (258)
+// 83.4 / 101.9, 2048 (344) 91.2 / 102.7, 2304 (387) 123.3 / 112.3, 3100 (559) 137.1 / 149.6, 4608 (774) 199.4 / 195.5,
+// 6100 (1032) 251.1 / 241.3; 4096 x 4096 at N = 4096 (256) 74.5 / 68.3; 8192 x 8192 at N = 1024 (128) 76.0 / 94.2, 1100 (160)
+// 110.3 / 95.7; 6304 x 768 at N = 6304 (625) 45.2 / 53.7; 28672 x 8192 at N = 8192 (3584) 1588 / 1378.
 hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s) {
-    if (((g.M + BM - 1) / BM) * ((g.N + 255) / 256) >= device_cus()) return launch<256>(g, s);
-    return launch<128>(g, s);
+    const int64_t cus = device_cus(), m = (g.M + BM - 1) / BM, wide = m * ((g.N + 255) / 256), narrow = m * ((g.N + 127) / 128);
+    const int64_t rounds = (wide + cus - 1) / cus;
+    return rounds >= 4 || narrow > (2 * rounds - 1) * cus ? launch<256>(g, s) : launch<128>(g, s);
 }
 
 }  // namespace sp24
