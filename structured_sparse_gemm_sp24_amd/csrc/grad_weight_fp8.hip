@@ -193,8 +193,21 @@ int grad_weight_parts(int64_t M, int64_t K, int64_t N) {
     return (int)(p < 1 ? 1 : p);
 }
 
+// The 256 x 256 kernel (one workgroup a compute unit) where its rounds of the chip are full enough: in one round, where the
+// tiles of 128 x 128 would take more than one of their own (two workgroups a compute unit); in two, from two thirds full;
+// always from three. Measured (us, 128 wide / 256 wide; tiles of 256 x 256): 2816 x 2816 over 8192 tokens (121) 160 / 202, 2048
+// x 4096 over 4096 (128) 98 / 113, 768 x 11008 over 8192 (129) 232 / 202, 4096 x 2304 over 4096 (144) 134 / 115, 4096 x
+// 4096 over 4096 (256) 165 / 122; 5120 x 4096 over 4096 (320) 199 / 220, 5632 x 4096 over 2048 (352) 131 / 127, 5120 x
+// 5120 over 2048 (400) 151 / 127; 11008 x 4096 over 4096 (688) 427 / 334.
+static bool grad_weight_takes_tiled(int64_t M, int64_t K) {
+    const int64_t cus = device_cus(), big = ((M + 255) / 256) * ((K + 255) / 256);
+    const int64_t small = ((M + BT - 1) / BT) * ((K + BT - 1) / BT), rounds = (big + cus - 1) / cus;
+    if (rounds == 1) return small > 2 * cus;
+    return 3 * big >= 2 * cus * rounds;
+}
+
 hipError_t launch_grad_weight(const Fp8GradArgs& g, hipStream_t s) {
-    if (((g.M + 255) / 256) * ((g.K + 255) / 256) >= 200) return launch_grad_weight_tiled(g, s);
+    if (grad_weight_takes_tiled(g.M, g.K)) return launch_grad_weight_tiled(g, s);
     const int parts = grad_weight_parts(g.M, g.K, g.N);
     Args a;
     a.dY = static_cast<const char*>(g.dY); a.X = g.X; a.xs = g.xs;
