@@ -1,25 +1,33 @@
 // Sparse x dense product in 8-bit floating point for many tokens, with a scale for each block of 128.
 //
-// Workgroup tile 256 (M) x 128 (N), four waves of 128 x 64 = 8 x 4 fragments of v_smfmac_f32_16x16x128_fp8_fp8; two
-// workgroups per compute unit (two waves a SIMD), so that one's epilogue and scaling run beside the other's matrix
-// instructions. K advances 128 dense columns a stage -- one block of scales, one matrix instruction a fragment --
-// through two LDS stage buffers of 36 KB:
+// Workgroup tile 256 (M) x 256 (N) with eight waves, or 256 x 128 with four and two workgroups a compute unit; either way two
+// waves a SIMD, of 128 x 64 = 8 x 4 fragments of v_smfmac_f32_16x16x128_fp8_fp8, so that one's scaling and epilogue run
+// beside the other's matrix instructions. K advances 128 dense columns a stage -- one block of scales, one matrix
+// instruction a fragment -- through two LDS stage buffers of 52 or 36 KB:
 //   A (compressed values): one 1 KB tile per 16-row block, already in the operand's lane order;
 //   metadata: one 256 B tile per block (lane l's 32-bit index at 4 l);
-//   B (codes of X): 128 token rows of 128 bytes; a lane's operand is the two 16-byte units q and q + 4 of its token's
+//   B (codes of X): the tile's token rows of 128 bytes; a lane's operand is the two 16-byte units q and q + 4 of its token's
 //     row, and unit u of row n is stored at u ^ ((n >> 1) & 7) ^ 4 (n & 1), which keeps the reads free of bank
 //     conflicts and each 4 lanes of a load on one 64-byte run.
 // The scales ride on the accumulators (Horner's rule). With e_b the exponent of block b's two scales, which depends on
 // the lane's token and the wave's 128 rows, an accumulator holds the sum so far in units of 2^e_b: before block b's
 // matrix instruction adds its products it is multiplied by 2^(e_(b-1) - e_b), exactly, and the last unit is put back
 // in the epilogue. That is four multiplications a fragment and stage; a product from zero and four fused multiply-adds
-// into a second accumulator are six instructions and four registers more, and measured 466 us against ... on
-// 8192^3. A block whose unit is 2^-64 or less of the largest before it in its sum is left out (its token's codes
+// into a second accumulator are six instructions and four registers more, and measured 466 us against 392 on 8192^3
+// (128-wide tiles both). A block whose unit is 2^-64 or less of the largest before it in its sum is left out (its token's codes
 // read as zeros), so that no accumulator can overflow: what it would add is below 2^-40 of that largest unit.
 //
 // Loads are buffer loads with LDS destination whose whole byte offset is in the range-checked VGPR operand: rows past
 // M and N, 16-byte units past K (inside a row what follows may be NaN codes, which zero weights would not cancel) and
 // the loads issued past the workgroup's last tile return zeros.
+//
+// The scales themselves are fetched eight stages at a time, a word each, into a buffer of their own.
+//
+// 28672 x 8192 on 8192 tokens: 1344 to 1380 us, 2.8 dense-equivalent PFLOP/s. What bounds it is a SIMD's issue: for each
+// matrix instruction of 16 cycles it issues about seven others of four, the four multiplications among them, for the
+// most part not beside the other wave's matrix instructions, since the stage's barrier keeps the eight waves in step.
+// Matrix cores are busy 31 % of the cycles at the 2.0 GHz that the chip holds under this load. HBM is not near: 2.1 GB
+// fetched a call, 1.5 TB/s.
 //
 // Persistent: a workgroup walks its tiles (neighbouring tiles on the same XCD at the same time, groups of 8
 // tile-rows) with the LDS pipeline continued across tiles.
