@@ -47,7 +47,10 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
     const __amdgpu_buffer_rsrc_t rA = rsrc(a.values + b0 * T * 1024, blocks * T * 1024);
     const __amdgpu_buffer_rsrc_t rM = rsrc(a.meta + b0 * T * 256, blocks * T * 256);
     const __amdgpu_buffer_rsrc_t rX = rsrc(a.X + n0 * a.ldx, (tokens - 1) * a.ldx + a.K);
-    const uint8_t* ws = a.ws + (b0 >> 3) * T;  // R divides 8: one row of weight scales
+    // eight row blocks share a row of weight scales; where R does not divide 8 the workgroup's last ones may be of the next
+    constexpr bool TWO = 8 % R != 0;
+    const uint8_t* ws = a.ws + (b0 >> 3) * T;
+    const uint8_t* ws2 = a.ws + ((b0 + blocks - 1) >> 3) * T;
     uint32_t xo[NF];
     const uint8_t* xs[NF];  // tokens past N take the last one's scales: their products are zeros, and not stored
 #pragma unroll
@@ -69,13 +72,14 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
         i32x4 av[U][R];
         int iv[U][R];
         i32x8 bv[U][NF];
-        uint32_t sx[U][NF], sw[U];
+        uint32_t sx[U][NF], sw[U], sw2[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const bool in = t + u < t1;
             const int tc = in ? t + u : t;  // scales of tiles past the range: any valid one (their products are zeros)
             const int k0 = (t + u) * KT + 16 * q;
             sw[u] = ws[tc];
+            if constexpr (TWO) sw2[u] = ws2[tc];
 #pragma unroll
             for (int f = 0; f < NF; f++) sx[u][f] = xs[f][tc];
 #pragma unroll
@@ -98,9 +102,11 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
         for (int u = 0; u < U; u++)
 #pragma unroll
             for (int f = 0; f < NF; f++) {
-                const float s = __builtin_amdgcn_ldexpf(scale_value(sx[u][f]), (int)sw[u] - 127);
+                const float x = scale_value(sx[u][f]), s1 = __builtin_amdgcn_ldexpf(x, (int)sw[u] - 127);
+                const float s2 = TWO ? __builtin_amdgcn_ldexpf(x, (int)sw2[u] - 127) : s1;
 #pragma unroll
                 for (int i = 0; i < R; i++) {
+                    const float s = TWO && ((b0 + i) >> 3) != (b0 >> 3) ? s2 : s1;
                     const f32x4 p = __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(av[u][i], bv[u][f], f32x4{0.f, 0.f, 0.f, 0.f}, iv[u][i], 0, 0);
 #pragma unroll
                     for (int e = 0; e < 4; e++) acc[i][f][e] = fmaf(p[e], s, acc[i][f][e]);
@@ -163,13 +169,19 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
 
 // Row blocks a workgroup (R), tiles a request (U) and waves (S), measured on MI355X with weights rotated beyond the
 // Infinity Cache (us):
-//  one fragment: 4096 x 4096 (256 row blocks) at N = 1 / 8 / 16: 4.4 / 5.0 / 5.9 with R = 1; 11008 x 4096 (688) at N = 1 /
-//    8: 8.7 / 9.0 with R = 2 against 8.5 / 10.4 with 1, at N = 16 10.1 with R = 4 against 12.8; 28672 x 8192 (1792) at N
-//    = 1 / 8: 29.4 / 31.1 with R = 2, at N = 16 33.0 with R = 8 against 35.5 with 4;
-//  two: 4096 x 4096 8.6 (R = 1) against 10.4; 11008 x 4096 12.4 (R = 4) against 15.6 (R = 2), 28672 x 8192 37.8 against 53.8;
-//  three: 4096 x 4096 11.3 (R = 1), 11008 x 4096 14.3 (R = 4), 28672 x 8192 47.8 (R = 4);
-//  four, and groups of 64 tokens: the largest R that still gives every compute unit a workgroup (4096 x 4096 at N = 64 14.4
-//    with R = 1 against 16.8 with 4, at N = 100 15.4 with 2, at N = 200 16.9 with 4 against 26.3 with 2).
+//  R is the least of 1, 2 and 3 that leaves at most one workgroup a compute unit, and 4 (8 with one fragment) beyond; the
+//  fewer, the more often each workgroup's X is read again, and at most 8 tokens are too few for that to count:
+//  one fragment: 4096 x 4096 (256 row blocks) at N = 1 / 8 / 16 4.4 / 5.0 / 5.9 with R = 1; 8192 x 8192 (512) at N = 1 / 8
+//    9.8 / 11.9 with R = 1, 10.9 / 11.3 with 2, at N = 16 11.8 with R = 2 against 15.4 with 1; 11008 x 4096 (688) at N = 1 / 8
+//    8.7 / 9.0 with R = 2 against 8.5 / 10.4 with 1, at N = 16 9.3 with R = 3 against 10.0 with 4; 14336 x 4096 (896) at N =
+//    16 10.8 with R = 4 against 12.7 with 3; 28672 x 8192 (1792) at N = 1 / 8 29.4 / 31.1 with R = 2, at N = 16 33.0 with R
+//    = 8 against 35.5 with 4;
+//  two: 4096 x 4096 8.4 with R = 1 against 9.2 with 2, 8192 x 8192 15.9 with 2 against 24.8 with 1, 11008 x 4096 11.7 with 3
+//    against 12.1 with 4, 28672 x 8192 37.8 with 4 against 53.8 with 2;
+//  three: 4096 x 4096 10.3 with R = 1 against 11.5 with 2, 8192 x 8192 20.8 with 2 against 31.9 with 1, 11008 x 4096 13.7
+//    with 3 against 14.4 with 4, 28672 x 8192 40.9 with 4 against 51.5 with 3;
+//  four, and groups of 64 tokens: 4096 x 4096 at N = 64 14.4 with R = 1 against 16.8 with 4, at N = 100 15.4 with 2, at N =
+//    190 17.2 with 4 against 26.8 with 3 (258 workgroups); 11008 x 4096 at N = 64 17.1 with 3 against 18.1 with 4.
 // The groups stream the weight once each, from L2 after the first; the tiled kernel reads it once but fills the chip
 // only with many tiles. Up to 2.25 workgroups of 64 x 64 a compute unit this one is the faster (4096 x 4096 at N = 512, 2:
 // 28.9 against 37 us; 11008 x 4096 at N = 200, 2.7: 40.7 against 38.8; 28672 x 8192 at N = 64, 1.75: 56 against 71, at N =
@@ -177,16 +189,28 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s) {
     const int64_t nb = (g.M + 15) / 16, groups = (g.N + 63) / 64, cus = device_cus();
     if (4 * ((nb + 3) / 4) * groups > 9 * cus && g.N > 64) return launch_gemm_fp8_tiled(g, s);
-    const bool small = nb <= 2 * cus;
+    int per = 1;  // the least R, up to 5, with at most one workgroup a compute unit
+    while (per < 5 && (nb + per - 1) / per * groups > cus) per++;
+    if (g.N <= 8) return per <= 2 ? launch<1, 1, 4, 4>(g, s) : launch<1, 2, 2, 4>(g, s);
     if (g.N <= 16) {
-        if (small) return launch<1, 1, 4, 4>(g, s);
-        if (g.N <= 8) return launch<1, 2, 2, 4>(g, s);
-        return nb <= 4 * cus ? launch<1, 4, 4, 8>(g, s) : launch<1, 8, 2, 8>(g, s);
+        if (per <= 1) return launch<1, 1, 4, 4>(g, s);
+        if (per <= 2) return launch<1, 2, 2, 4>(g, s);
+        if (per <= 3) return launch<1, 3, 2, 4>(g, s);
+        return per <= 4 ? launch<1, 4, 4, 8>(g, s) : launch<1, 8, 2, 8>(g, s);
     }
-    if (g.N <= 32) return small ? launch<2, 1, 2, 4>(g, s) : launch<2, 4, 1, 8>(g, s);
-    if (g.N <= 48) return small ? launch<3, 1, 2, 4>(g, s) : launch<3, 4, 2, 4>(g, s);
-    if (nb * groups <= cus) return launch<4, 1, 2, 4>(g, s);
-    return nb * groups <= 2 * cus ? launch<4, 2, 2, 4>(g, s) : launch<4, 4, 2, 4>(g, s);
+    if (g.N <= 32) {
+        if (per <= 1) return launch<2, 1, 2, 4>(g, s);
+        if (per <= 2) return launch<2, 2, 2, 4>(g, s);
+        return per <= 3 ? launch<2, 3, 1, 8>(g, s) : launch<2, 4, 1, 8>(g, s);
+    }
+    if (g.N <= 48) {
+        if (per <= 1) return launch<3, 1, 2, 4>(g, s);
+        if (per <= 2) return launch<3, 2, 2, 8>(g, s);
+        return per <= 3 ? launch<3, 3, 2, 4>(g, s) : launch<3, 4, 2, 4>(g, s);
+    }
+    if (per <= 1) return launch<4, 1, 2, 4>(g, s);
+    if (per <= 2) return launch<4, 2, 2, 4>(g, s);
+    return per <= 3 ? launch<4, 3, 2, 4>(g, s) : launch<4, 4, 2, 4>(g, s);
 }
 
 }  // namespace sp24

@@ -381,6 +381,16 @@ def test_gemm_nan_and_scale_range(N):
     assert (np.abs(got - want) <= gemm_bound(x64, w64, want, ref.UB) + K * 2.0 ** -133).all()
 
 
+@pytest.mark.parametrize("N", [2, 11, 16, 25, 43, 64, 130])
+@pytest.mark.parametrize("M", [2100, 4100, 6000, 8170, 10000, 12200])
+def test_gemm_row_blocks(M, N):
+    """One to three row blocks a workgroup, and three that may lie in two rows of weight scales."""
+    say(f"gemm fp8 row blocks {M} N {N}")
+    w, x, xs, want = int_case(M, 272, N, 3)
+    y = sp.sp24_gemm_fp8(*w, M, x, xs)
+    assert torch.equal(y.cpu(), torch.from_numpy(want).to(torch.bfloat16))
+
+
 def test_gemm_counts_kept_weights():
     """Ones everywhere: Y counts the kept weights, whatever the tiling (exact)."""
     for M, K, N in ((48, 400, 5), (300, 144, 90), (260, 1040, 260)):
