@@ -18,8 +18,8 @@
  * Conventions are those of sp24.h (caller-owned device memory, asynchronous on `stream`, validated on the host
  * before any launch, K a positive multiple of 16, M, N >= 1). In addition: base pointers of matrices are 16-byte
  * aligned; a pitch in bytes is a multiple of 16, except that of an output Y (any pitch) and of scales; pitches are
- * below 2^23 elements, those of scales below 2^22; K is at most 2^20, N below 2^31, M at most 2^22 (a launch that
- * would need 2^24 workgroups or more is SP24_ERR_SHAPE). Results are deterministic: no sum depends on the order in
+ * below 2^23 elements, those of scales below 2^22; K is at most 2^20, N below 2^31, M at most 2^22 (what would need
+ * 2^32 threads or more in one launch is SP24_ERR_SHAPE). Results are deterministic: no sum depends on the order in
  * which workgroups run.
  */
 #ifndef SP24_FP8_H
