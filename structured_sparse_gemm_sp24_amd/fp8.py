@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 
 import torch
@@ -50,13 +51,18 @@ def bind(lib: ctypes.CDLL) -> None:
 
 
 def _on_device(fn):
-    """Runs fn on its first operand's device, a GPU."""
+    """Runs fn on its first operand's device, a GPU; that operand too may be given by its name."""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, **kw):
+    def call(*args, **kw):
+        if not args and name not in kw:
+            raise TypeError(f"{fn.__name__}() needs {name}")
+        first = args[0] if args else kw[name]
         if not first.is_cuda:
             raise ValueError("sp24 operates on device tensors only")
         with torch.cuda.device(first.device):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 

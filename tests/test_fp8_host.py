@@ -154,3 +154,17 @@ def test_plain_codes():
     v = np.random.default_rng(0).uniform(-448, 448, 10000).astype(np.float32)
     assert np.array_equal(ref.e4m3(v.astype(np.float64)), torch.from_numpy(v).to(torch.float8_e4m3fn).double().numpy())
     assert list(ref.scale_exp(np.array([0.0, 448.0, 448.001, 224.0, 224.001, 1e-45]))) == [-127, 0, 1, -1, 0, -127]
+
+
+def test_binding_takes_keywords():
+    """Every operand can be given by its name, the first one too (host tensors: refused as such, not as a wrong call)."""
+    x = torch.zeros(16, 128, dtype=torch.bfloat16)
+    codes, scales = x.to(torch.float8_e4m3fn), torch.zeros(16, 1, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    values, meta, w_scales = torch.zeros(1024).to(torch.float8_e4m3fn), torch.zeros(256, dtype=torch.uint8), scales[:1]
+    for call in (lambda: sp.sp24_prune_compress_fp8(W=x), lambda: sp.sp24_decompress_fp8(values=values, meta=meta, w_scales=w_scales, M=16, K=128),
+                 lambda: sp.sp24_decompress_fp8(M=16, K=128, w_scales=w_scales, meta=meta, values=values), lambda: sp.sp24_quant_fp8(X=x),
+                 lambda: sp.sp24_rmsnorm_fp8(X=x, gamma=x[0]), lambda: sp.sp24_rmsnorm_backward(dY=x, H=x, rstd=x[:, 0].float(), gamma=x[0]),
+                 lambda: sp.sp24_gemm_fp8(values=values, meta=meta, w_scales=w_scales, M=16, X=codes, x_scales=scales),
+                 lambda: sp.sp24_grad_weight_fp8(dY=x, X=codes, x_scales=scales)):
+        with pytest.raises(ValueError, match="device tensors only"):
+            call()
