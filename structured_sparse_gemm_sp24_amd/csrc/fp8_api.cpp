@@ -21,6 +21,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 bool is_float(int dt) { return dt == SP24_BF16 || dt == SP24_FP16 || dt == SP24_FP32; }
 int type_size(int dt) { return dt == SP24_FP32 ? 4 : 2; }
 int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+int64_t tiles_256(int64_t a, int64_t b) { return ((a + 255) / 256) * ((b + 255) / 256); }
 
 int check_nk(int64_t N, int64_t K, int64_t most_k) {
     return N < 1 || N > kMaxRows || K < 16 || K % 16 != 0 || K > most_k ? SP24_ERR_SHAPE : SP24_OK;
@@ -138,8 +139,9 @@ int sp24_gemm_fp8(const uint8_t* values, const uint8_t* meta, const uint8_t* w_s
     if (!values || !meta || !w_scales || !X || !x_scales || !Y) return SP24_ERR_NULL;
     if (out_dtype != SP24_BF16 && out_dtype != SP24_FP16) return SP24_ERR_DTYPE;
     SP24_TRY(check_nk(N, K, kMaxK));
-    // tiles of 256 x 128: one workgroup each where K is a single block
-    if (M < 1 || M > kMaxWeightRows || ((M + 255) / 256) * blocks_of(N) > kMaxGrid) return SP24_ERR_SHAPE;
+    if (M < 1 || M > kMaxWeightRows) return SP24_ERR_SHAPE;
+    // tiles of 256 x 128 with 256 threads or of 256 x 256 with 512: one workgroup each where K is a single block
+    if (((M + 255) / 256) * blocks_of(N) > kMaxGrid || tiles_256(M, N) > kMaxGrid / 2) return SP24_ERR_SHAPE;
     SP24_TRY(check_matrix(X, K, ldx, 1));
     SP24_TRY(check_scales(K, lds));
     if (ldy < M || ldy >= kMaxPitch) return SP24_ERR_SHAPE;
@@ -155,7 +157,7 @@ int sp24_gemm_fp8(const uint8_t* values, const uint8_t* meta, const uint8_t* w_s
 int sp24_grad_weight_fp8_bytes(int64_t M, int64_t K, int64_t N, int64_t* bytes) {
     if (!bytes) return SP24_ERR_NULL;
     SP24_TRY(check_nk(N, K, kMaxK));
-    if (M < 1 || M > kMaxWeightRows) return SP24_ERR_SHAPE;
+    if (M < 1 || M > kMaxWeightRows || tiles_256(M, K) > kMaxGrid / 2) return SP24_ERR_SHAPE;
     const int parts = sp24::grad_weight_parts(M, K, N);
     *bytes = parts > 1 ? (int64_t)parts * M * K * 4 : 0;
     return SP24_OK;
@@ -167,7 +169,8 @@ int sp24_grad_weight_fp8(const void* dY, int64_t N, int64_t M, int64_t lddy, con
     if (!dY || !X || !x_scales || !dW) return SP24_ERR_NULL;
     if (out_dtype != SP24_BF16 && out_dtype != SP24_FP32) return SP24_ERR_DTYPE;
     SP24_TRY(check_nk(N, K, kMaxK));
-    if (M < 1 || M > kMaxWeightRows) return SP24_ERR_SHAPE;
+    // one workgroup of 512 threads a tile (small weights, far below the limit, take smaller tiles)
+    if (M < 1 || M > kMaxWeightRows || tiles_256(M, K) > kMaxGrid / 2) return SP24_ERR_SHAPE;
     if (!workspace && sp24::grad_weight_parts(M, K, N) > 1) return SP24_ERR_NULL;
     SP24_TRY(check_matrix(dY, M, lddy, 2));
     SP24_TRY(check_matrix(X, K, ldx, 1));

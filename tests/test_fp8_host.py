@@ -168,3 +168,16 @@ def test_binding_takes_keywords():
                  lambda: sp.sp24_grad_weight_fp8(dY=x, X=codes, x_scales=scales)):
         with pytest.raises(ValueError, match="device tensors only"):
             call()
+
+
+def test_launch_limits(lib):  # noqa: F811
+    """What would need 2^32 threads or more in one launch is a shape error before any HIP call."""
+    wide = dict(M=1 << 22, K=16, ldx=16, ldy=1 << 22)
+    # 2^14 tile rows x 512 tiles of 256 tokens, 512 threads each: 2^32
+    assert lib.sp24_gemm_fp8(*changed(GEMM, **wide, N=511 * 256 + 1)) == SHAPE
+    n = ctypes.c_int64(-1)
+    # 2^14 x 2^9 and 2^14 x 2^12 tiles of 256 x 256, 512 threads each: 2^32 and 2^35
+    for K in (511 * 256 + 16, 1 << 20):
+        assert lib.sp24_grad_weight_fp8_bytes(1 << 22, K, 64, ctypes.byref(n)) == SHAPE
+        assert lib.sp24_grad_weight_fp8(*changed(GRAD, N=64, M=1 << 22, lddy=1 << 22, K=K, ldx=K, lds=1 << 13, ldw=K)) == SHAPE
+    assert lib.sp24_grad_weight_fp8_bytes(1 << 22, 511 * 256, 64, ctypes.byref(n)) == 0 and n.value == 0
