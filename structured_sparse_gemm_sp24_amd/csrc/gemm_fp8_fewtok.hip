@@ -6,7 +6,8 @@
 // ranges. A wave requests U tiles' operands at a time before their products: per lane and row block the 16-byte run
 // of its slot in the value tile and its 32-bit index, per fragment the two 16-byte runs of its token's row that are
 // the operand's halves (k0 + 16 q and k0 + 64 + 16 q), and the scales of the tile. A tile's product starts from
-// zero; then acc = fma(product, 2^(x scale + w scale), acc), the power of two formed once a fragment and tile.
+// zero; then acc = fma(product, 2^(x scale + w scale), acc), the power of two formed once a fragment and tile (NaN
+// where either scale is).
 //
 // Reads go through buffer descriptors: row blocks past M, tokens past N, runs past K (inside a row as well: what
 // follows there may be a NaN code, which a zero weight would not cancel) and tiles past a wave's range read zeros.
@@ -102,8 +103,7 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
         for (int u = 0; u < U; u++)
 #pragma unroll
             for (int f = 0; f < NF; f++) {
-                const float x = scale_value(sx[u][f]), s1 = __builtin_amdgcn_ldexpf(x, (int)sw[u] - 127);
-                const float s2 = TWO ? __builtin_amdgcn_ldexpf(x, (int)sw2[u] - 127) : s1;
+                const float x = scale_value(sx[u][f]), s1 = x * scale_value(sw[u]), s2 = TWO ? x * scale_value(sw2[u]) : s1;
 #pragma unroll
                 for (int i = 0; i < R; i++) {
                     const float s = TWO && ((b0 + i) >> 3) != (b0 >> 3) ? s2 : s1;

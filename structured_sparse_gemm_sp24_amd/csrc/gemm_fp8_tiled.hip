@@ -264,7 +264,7 @@ __device__ __forceinline__ void advance(Units& u, const Scales& s) {
         const int least = u.top[j] - 64, now = e > least ? e : least;
         u.skip |= (uint32_t)(e < least) << j;
         const int d = u.e[j] - now + 127;  // at most 64 + 127
-        u.f[j] = s.x[j] == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(d > 0 ? d : 0) << 23);
+        u.f[j] = max(s.x[j], s.w) == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(d > 0 ? d : 0) << 23);
         u.e[j] = now;
     }
 }
