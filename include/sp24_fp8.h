@@ -76,9 +76,8 @@ int sp24_decompress_fp8(const uint8_t* values, const uint8_t* meta, const uint8_
  *   2^-13 of the largest one (measured), far below the codes' own 2^-4 and invisible after rounding to 16 bits; an
  *   FP32 result would promise more than that, so none is offered.
  * A NaN scale of x makes its token's row NaN, one of the weight its 128 output channels. The product of two scales
- * must be below 2^128. With many tokens a block whose product of scales is less than 2^-64 of the largest one before it
- * in its sum is left out (what it would add is below 2^-40 of that larger unit); for blocks within 2^64 of each other
- * results depend on the sizes, which choose the kernel, only through the order of the fp32 sums. */
+ * must be below 2^128; one below 2^-149 may count as zero. Results depend on the sizes, which choose the kernel, only
+ * through the order of the fp32 sums, however far apart a token's scales are. */
 int sp24_gemm_fp8(const uint8_t* values, const uint8_t* meta, const uint8_t* w_scales, int64_t M, int64_t K,
                   const uint8_t* X, int64_t N, int64_t ldx, const uint8_t* x_scales, int64_t lds, void* Y, int out_dtype,
                   int64_t ldy, void* stream);

@@ -14,8 +14,10 @@
 // matrix instruction adds its products it is multiplied by 2^(e_(b-1) - e_b), exactly, and the last unit is put back
 // in the epilogue. That is four multiplications a fragment and stage; a product from zero and four fused multiply-adds
 // into a second accumulator are six instructions and four registers more, and measured 466 us against 392 on 8192^3
-// (128-wide tiles both). A block whose unit is 2^-64 or less of the largest before it in its sum is left out (its token's codes
-// read as zeros), so that no accumulator can overflow: what it would add is below 2^-40 of that largest unit.
+// (128-wide tiles both). Accumulators neither overflow nor lose bits this way while a token's units lie within 2^64 of each
+// other. Where they do not (the wave keeps the least and the largest), the wave sums that tile again after its last one,
+// from memory, adding each block's products with their own scale. Blocks of zeros, whose scale is the least there is, keep
+// the unit that they meet and do not count.
 //
 // Loads are buffer loads with LDS destination whose whole byte offset is in the range-checked VGPR operand: rows past
 // M and N, 16-byte units past K (inside a row what follows may be NaN codes, which zero weights would not cancel) and
@@ -57,6 +59,7 @@ struct Cfg {
 };
 constexpr int GROUP_M = 8;
 constexpr uint32_t OOR = 0x80000000u;  // a byte offset past every record count
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 struct Args {
     const uint8_t *values, *meta, *ws, *X, *xs;
     void* Y;
@@ -121,6 +124,7 @@ struct Desc {
     i32x4 rA, rM;
     const uint8_t* xs;  // the first token's scales
     int xs_bytes;       // from there to the end of the scales
+    int tokens;         // from the first token to the last of all; those past it take its scales
     const uint8_t* x;  // first token of the wave's rows to load
     int64_t xbytes;    // from there to the end of X, 0 for no tile
     int wrow;          // byte offset of the wave's row of weight scales
@@ -135,10 +139,12 @@ __device__ __forceinline__ Desc desc_of(const Args& a, const Tile& t, int wave, 
     d.rM = make_rsrc(a.meta + (t.m0 / 16) * tiles * 256, t.valid ? blocks * tiles * 256 : 0);
     const int64_t sb = (a.N - 1 - t.n0) * a.lds + a.S;
     d.xs = a.xs + t.n0 * a.lds;
+    d.tokens = (int)(a.N - 1 - t.n0 < BN ? a.N - 1 - t.n0 : BN);
     d.xs_bytes = !t.valid ? 0 : (int)(sb > 0x7FFFFFFF ? 0x7FFFFFFF : sb);
     d.x = a.X + n1 * a.ldx;
     d.xbytes = t.valid ? (a.N - 1 - n1) * a.ldx + a.K : 0;
-    d.wrow = (int)((t.m0 + wm0) >> 7) * a.S;
+    const int64_t m = t.m0 + wm0 < a.M ? t.m0 + wm0 : a.M - 1;
+    d.wrow = (int)(m >> 7) * a.S;
     return d;
 }
 
@@ -227,8 +233,8 @@ __device__ __forceinline__ void load_chunk(uint32_t lds, const Args& a, const De
     const i32x4 rS = make_rsrc(d.xs, d.xs_bytes);
 #pragma unroll
     for (int h = 0; h < 4; h++) {
-        const int t = 4 * wave + h;
-        dma1(lds + t * 256, (uint32_t)((8 * t + (lane & 7)) * (int)a.lds + s + (lane >> 3)), rS);
+        const int t = 4 * wave + h, n = 8 * t + (lane & 7);
+        dma1(lds + t * 256, (uint32_t)((n < d.tokens ? n : d.tokens) * (int)a.lds + s + (lane >> 3)), rS);
     }
 }
 
@@ -236,37 +242,33 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* base, int 
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, bytes, 0x00020000);
 }
 
-// The wave's weight scale of stage s of tile d; rows past M read zero.
+// The wave's weight scale of stage s of tile d.
 __device__ __forceinline__ uint32_t load_w(const Args& a, const Desc& d, int s) {
     const __amdgpu_buffer_rsrc_t rw = rsrc(a.ws, (int)((a.M + 127) / 128 * a.S));  // below 2^28 (M <= 2^22, K <= 2^20)
     return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rw, d.wrow, s, 0);
 }
 
-// The running units of a lane's four tokens: exponents of the current and of the largest unit (biases included), and
-// the stage's factors 2^(previous - current).
+// The running units of a lane's four tokens, two in a register: exponent of the current one, the least and the largest so
+// far (biases included); and the stage's factors 2^(previous - current).
 struct Units {
-    int e[FN], top[FN];
+    i16x2 e[FN / 2], lo[FN / 2], hi[FN / 2];
     float f[FN];
-    uint32_t skip;  // bit j: column j's block is left out
+    bool apart;  // a block that the running unit cannot hold
 };
+constexpr int SPAN = 64;
 
 __device__ __forceinline__ void reset(Units& u) {
 #pragma unroll
-    for (int j = 0; j < FN; j++) u.e[j] = u.top[j] = 0;
+    for (int p = 0; p < FN / 2; p++) u.e[p] = i16x2{0, 0}, u.lo[p] = i16x2{8192, 8192}, u.hi[p] = i16x2{-8192, -8192};
+    u.apart = false;
 }
 
-__device__ __forceinline__ void advance(Units& u, const Scales& s) {
-    u.skip = 0;
+// Whether the wave's tile has to be summed block by block.
+__device__ __forceinline__ bool far_apart(const Units& u) {
+    bool far = u.apart;
 #pragma unroll
-    for (int j = 0; j < FN; j++) {
-        const int e = (int)(s.x[j] + s.w);
-        u.top[j] = e > u.top[j] ? e : u.top[j];
-        const int least = u.top[j] - 64, now = e > least ? e : least;
-        u.skip |= (uint32_t)(e < least) << j;
-        const int d = u.e[j] - now + 127;  // at most 64 + 127
-        u.f[j] = max(s.x[j], s.w) == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(d > 0 ? d : 0) << 23);
-        u.e[j] = now;
-    }
+    for (int j = 0; j < FN; j++) far |= u.hi[j / 2][j % 2] - u.lo[j / 2][j % 2] > SPAN;
+    return __builtin_amdgcn_ballot_w64(far) != 0;
 }
 
 struct AFrags {
@@ -320,6 +322,9 @@ __device__ __forceinline__ void last_columns(const StageLoads<BN>& loads, const 
     }
 }
 
+// Nonzero where one of 16 codes is a number other than zero, or NaN.
+__device__ __forceinline__ uint32_t any_code(const i32x4& v) { return (uint32_t)(v[0] | v[1] | v[2] | v[3]) & 0x7F7F7F7Fu; }
+
 __device__ __forceinline__ void read_a(uint32_t buf, const LaneOffsets& o, AFrags& fa) {
     const lds_char *pa = stage_addr(buf, o.a), *pm = stage_addr(buf, o.m);
 #pragma unroll
@@ -338,11 +343,52 @@ struct Stage {
     int chunk;  // LDS area of the current chunk of scales
 };
 
-// Zeroes the codes of tokens whose block is left out in column j.
-__device__ __forceinline__ void skip(i32x8& b, uint32_t mask, int j) {
-    const int keep = (int)((mask >> j) & 1u) - 1;
+// The units of a stage whose operands are in `buf` and g. The rare scales are the NaN, which makes the sum NaN, and
+// the least one: that of a block of zeros (it keeps the unit) or of numbers below 2^-118 (the sum is made again).
+__device__ __forceinline__ void advance(Stage& g, uint32_t buf, const LaneOffsets& o) {
+    Units& u = g.u;
+    const uint32_t w = g.sc.w;
+    i16x2 e[FN / 2], lo[FN / 2], hi[FN / 2];
+    uint32_t least = w, most = w, nan = 0;
 #pragma unroll
-    for (int w = 0; w < 8; w++) b[w] &= keep;
+    for (int j = 0; j < FN; j++) least = min(least, g.sc.x[j]), most = max(most, g.sc.x[j]);
+#pragma unroll
+    for (int p = 0; p < FN / 2; p++) {
+        e[p] = __builtin_bit_cast(i16x2, g.sc.x[2 * p] | (g.sc.x[2 * p + 1] << 16)) + __builtin_bit_cast(i16x2, w | (w << 16));
+        lo[p] = __builtin_elementwise_min(u.lo[p], e[p]);
+        hi[p] = __builtin_elementwise_max(u.hi[p], e[p]);
+    }
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(least == 0u || most == 255u) != 0, 0)) {
+        uint32_t some = 0;
+#pragma unroll
+        for (int i = 0; i < FM; i++) some |= any_code(g.fa.a[i]);
+        const bool weights = __builtin_amdgcn_ballot_w64(some != 0) != 0;
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+            const uint32_t x = g.sc.x[j];
+            const bool is_nan = max(x, w) == 255u, zero = !is_nan && min(x, w) == 0u;
+            const i32x4 first = *reinterpret_cast<lds_i32x4*>(stage_addr(buf, o.b0) + j * 2048);
+            const i32x4 last = *reinterpret_cast<lds_i32x4*>(stage_addr(buf, o.b1) + j * 2048);
+            u.apart |= zero && weights && any_code(first | last) != 0;
+            nan |= (uint32_t)is_nan << j;
+            if (is_nan || zero) {
+                e[j / 2][j % 2] = u.e[j / 2][j % 2];
+                lo[j / 2][j % 2] = u.lo[j / 2][j % 2];
+                hi[j / 2][j % 2] = u.hi[j / 2][j % 2];
+            }
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < FN / 2; p++) {
+        const i16x2 d = u.e[p] - e[p];
+        u.f[2 * p] = __builtin_amdgcn_ldexpf(1.f, d[0]);
+        u.f[2 * p + 1] = __builtin_amdgcn_ldexpf(1.f, d[1]);
+        u.e[p] = e[p], u.lo[p] = lo[p], u.hi[p] = hi[p];
+    }
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(nan != 0) != 0, 0)) {
+#pragma unroll
+        for (int j = 0; j < FN; j++) u.f[j] = (nan >> j) & 1u ? __uint_as_float(0x7FC00000u) : u.f[j];
+    }
 }
 
 __device__ __forceinline__ void read_x_scales(uint32_t area, int off, int s, Scales& sc) {
@@ -366,10 +412,9 @@ __device__ __forceinline__ void stage(const Args& a, const Desc& dc, const Desc&
         const bool in = s + CHUNK < S;
         load_chunk(chunks + (g.chunk ^ 1) * CHUNK_BYTES, a, in ? dc : dn, in ? s + CHUNK : 0, wave, lane);
     }
-    advance(g.u, g.sc);
+    advance(g, cb, o);
     g.sc.w = load_w(a, NEXT ? dc : dn, NEXT ? s + 1 : 0);  // landed by the wait below
     g.b2 = read_b(cb, o, 3);
-    if (__builtin_amdgcn_ballot_w64(g.u.skip & 3u)) skip(g.b0, g.u.skip, 0), skip(g.b1, g.u.skip, 1);
     rescale(acc[0][0], g.u.f[0]);
     __builtin_amdgcn_sched_barrier(0);
     column<0>(acc, g.fa, g.b0, g.u);
@@ -384,7 +429,6 @@ __device__ __forceinline__ void stage(const Args& a, const Desc& dc, const Desc&
     if constexpr (!Cfg<BN>::SPREAD) loads.issue_all(lo);
     if (!NEXT || ((s + 1) & (CHUNK - 1)) == 0) g.chunk ^= 1;
     read_x_scales(chunks + g.chunk * CHUNK_BYTES, o.s, NEXT ? s + 1 : 0, g.sc);
-    if (__builtin_amdgcn_ballot_w64(g.u.skip & 12u)) skip(g.b0, g.u.skip, 2), skip(g.b2, g.u.skip, 3);
     if constexpr (NEXT) {
         g.b1 = read_b(nb, o, 0);
         last_columns<BN, true>(loads, lo, acc, g.fa, g.b0, g.b2, g.u, stage_addr(nb, o.a), stage_addr(nb, o.m));
@@ -411,7 +455,7 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Uni
             for (int f = 0; f < 4; f++) {
                 f32x4 y = acc[4 * ig + f][j];
 #pragma unroll
-                for (int e = 0; e < 4; e++) y[e] = __builtin_amdgcn_ldexpf(y[e], u.e[j] - 254);
+                for (int e = 0; e < 4; e++) y[e] = __builtin_amdgcn_ldexpf(y[e], u.e[j / 2][j % 2] - 254);
                 v[f][0] = pack16<F16>(y[0], y[1]);
                 v[f][1] = pack16<F16>(y[2], y[3]);
             }
@@ -430,6 +474,60 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Uni
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+}
+
+// The wave's tile at (mw, nw) from memory: each block's products from zero and added with their own scale, 16 rows at a
+// time.
+template <bool F16>
+__device__ __forceinline__ void sum_apart(const Args& a, int64_t mw, int64_t nw) {
+    const int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));  // nothing kept for this
+    const int q = lane >> 4, r = lane & 15, S = a.S;
+    const int64_t xb = (a.N - 1 - nw) * a.ldx + a.K;
+    const __amdgpu_buffer_rsrc_t rX = rsrc(a.X + nw * a.ldx, (int)(xb > 0x7FFFFFFF ? 0x7FFFFFFF : xb));
+    const uint8_t* const ws = a.ws + (mw >> 7) * S;
+    uint32_t xo[FN], so[FN];
+#pragma unroll
+    for (int j = 0; j < FN; j++) {
+        const int64_t n = 16 * j + r, last = a.N - 1 - nw;
+        xo[j] = n <= last ? (uint32_t)(n * a.ldx + 16 * q) : OOR;
+        so[j] = (uint32_t)((n <= last ? n : last) * a.lds);
+    }
+#pragma unroll 1
+    for (int i = 0; i < FM && mw + 16 * i < a.M; i++) {
+        const uint8_t* const va = a.values + (mw / 16 + i) * S * 1024 + 16 * lane;
+        const uint8_t* const ma = a.meta + (mw / 16 + i) * S * 256 + 4 * lane;
+        f32x4 acc[FN];
+#pragma unroll
+        for (int j = 0; j < FN; j++) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int t = 0; t < S; t++) {
+            const int left = (int)a.K - t * BK - 16 * q;
+            const i32x4 v = *reinterpret_cast<const i32x4*>(va + t * 1024);
+            const int idx = *reinterpret_cast<const int*>(ma + t * 256);
+            const uint32_t w = ws[t];
+#pragma unroll
+            for (int j = 0; j < FN; j++) {
+                const uint32_t x = (a.xs + nw * a.lds + t)[so[j]], off = xo[j] + (uint32_t)(t * BK);
+                const i32x4 lo = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rX, (int)(left > 0 ? off : OOR), 0, 0));
+                const i32x4 hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rX, (int)(left > 64 ? off + 64u : OOR), 0, 0));
+                const i32x8 b = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                const f32x4 p = __builtin_amdgcn_smfmac_f32_16x16x128_fp8_fp8(v, b, f32x4{0.f, 0.f, 0.f, 0.f}, idx, 0, 0);
+                const float nan = max(x, w) == 255u ? __uint_as_float(0x7FC00000u) : 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; c++) acc[j][c] += __builtin_amdgcn_ldexpf(p[c] + nan, (int)(x + w) - 254);
+            }
+        }
+        const int64_t m = mw + 16 * i + 4 * q;
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+            const int64_t n = nw + 16 * j + r;
+            const uint32_t y[2] = {pack16<F16>(acc[j][0], acc[j][1]), pack16<F16>(acc[j][2], acc[j][3])};
+            uint16_t* const out = static_cast<uint16_t*>(a.Y) + n * a.ldy + m;
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                if (n < a.N && m + c < a.M) out[c] = (uint16_t)(y[c >> 1] >> (16 * (c & 1)));
+        }
+    }
 }
 
 template <int BN, bool F16>
@@ -470,6 +568,7 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
     read_x_scales(l0 + NBUF * STAGE_BYTES, o.s, 0, g.sc);
 
     int buf = 0;
+    uint64_t apart = 0;  // bit k % 64: the wave's tile k is summed block by block, after the others
     for (int k = 1;; k++) {
         read_a(l0 + buf * STAGE_BYTES, o, g.fa);
         g.b0 = read_b(l0 + buf * STAGE_BYTES, o, 0);
@@ -478,7 +577,8 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
         stage<BN, false>(a, dc, dn, S - 1, l0, buf, acc, g, o, wave, lane, lo);
         buf ^= 1;
         const int64_t mw = cur.m0 + wm0, nw = cur.n0 + wn0;
-        if (mw + WM <= a.M && nw + WN <= a.N && a.y_vec) store_tile<F16, true>(acc, g.u, a, mw, nw, lane);
+        if (__builtin_expect(far_apart(g.u), 0)) apart |= 1ull << ((k - 1) & 63);
+        else if (mw + WM <= a.M && nw + WN <= a.N && a.y_vec) store_tile<F16, true>(acc, g.u, a, mw, nw, lane);
         else store_tile<F16, false>(acc, g.u, a, mw, nw, lane);
         if (!next.valid) break;
 #pragma unroll
@@ -492,6 +592,11 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
         dn = desc_of<BN>(a, next, wave, wm0);
     }
     wait_vmcnt0();  // the zero-filling loads past the last tile have landed before the workgroup ends
+    for (int k = 0; apart != 0; k++) {
+        const Tile t = tile_of<BN>(a, p, k);
+        if (!t.valid) break;
+        if ((apart >> (k & 63)) & 1 && t.n0 + wn0 < a.N) sum_apart<F16>(a, t.m0 + wm0, t.n0 + wn0);
+    }
 }
 
 template <int BN>

@@ -1,5 +1,9 @@
-"""Scales of the 8-bit product at their extremes. Codes are small whole numbers, so every block's sum is exact in the
-matrix instruction and in fp32."""
+"""Scales of the 8-bit product at their extremes: NaN, far apart in either order, 2^-127, and those of blocks of zeros.
+
+Codes are small whole numbers, so every block's sum is exact in the matrix instruction and in fp32. Where all that a
+row of the weight keeps lies in blocks of one unit, its outputs are the rounded 64-bit result bit for bit, whatever
+the other blocks' scales are: what they add is zero. Elsewhere the largest unit decides and the result is within the
+roundings of T fp32 additions and of the output."""
 import numpy as np
 import pytest
 import torch
@@ -47,6 +51,16 @@ def product(w, sw, x, sx, dtype=torch.bfloat16):
     return ref.f64(sp.sp24_gemm_fp8(*weight(w, sw), w.shape[0], codes, e8m0(sx), out_dtype=dtype))
 
 
+def block_of_columns(b):
+    return slice(128 * b, min(K, 128 * b + 128))
+
+
+def scaled(w, sw, x, sx):
+    """The operands with their scales, in 64 bits."""
+    rows = np.repeat(2.0 ** (sw.astype(np.float64) - 127), 128, 0)[:w.shape[0]]
+    return w * np.repeat(rows, 128, 1)[:, :K], x * np.repeat(2.0 ** (sx.astype(np.float64) - 127), 128, 1)[:, :K]
+
+
 def rounded(y, dtype=torch.bfloat16):
     return ref.f64(torch.from_numpy(y).to(dtype))
 
@@ -70,3 +84,69 @@ def test_nan_weight_scale(M, N):
     dense = ref.f64(sp.sp24_decompress_fp8(*weight(w, sw), M, K, torch.float32))
     assert np.isnan(dense[128:256, 512:640]).any() and not np.isnan(dense[~bad]).any()
     assert not np.isnan(np.delete(dense, np.s_[512:640], 1)).any()
+
+
+# exponents of the scales of x in blocks 0 .. 9
+FAR = {
+    "large first": [80] + [0] * 9,
+    "large last": [-70] * 9 + [70],
+    "large in the middle": [0] * 5 + [90] + [0] * 4,
+    "small last": [0] * 9 + [-80],
+    "rising": [-90 + 20 * b for b in range(10)],
+    "falling": [90 - 20 * b for b in range(10)],
+    "up and down": [0, 70, -70, 70, -70, 0, 100, -100, 0, 65],
+    "across the limit": [0, 64, 0, 65, 0, -64, 0, -65, 63, 0],
+}
+
+
+@pytest.mark.parametrize("exponents", FAR.values(), ids=FAR.keys())
+@pytest.mark.parametrize("M,N", SIZES)
+def test_scales_far_apart(M, N, exponents):
+    """Some tokens with such scales among ordinary ones. Row m of the weight keeps only block m % 11 (or, at 10, all)."""
+    say(f"gemm fp8 far scales {M} N {N} {exponents}")
+    w, x = case(M, N, 1)
+    which = np.arange(M) % 11
+    for b in range(T):
+        w[:, block_of_columns(b)] *= ((which == b) | (which == 10))[:, None]
+    sw, sx = scale_bytes(M, N)
+    far = np.arange(N) % 97 == 2
+    sx[far] += np.array(exponents)
+    got = product(w, sw, x, sx)
+    wf, xf = scaled(w, sw, x, sx)
+    want = xf @ wf.T
+    assert np.array_equal(got[:, which < 10], rounded(want)[:, which < 10])
+    assert np.array_equal(got[~far], rounded(want)[~far])
+    bound = 1.01 * ref.UB * np.abs(want) + (T + 8) * ref.U32 * (np.abs(xf) @ np.abs(wf).T)
+    assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("M,N", SIZES)
+def test_blocks_of_zeros(M, N):
+    """Zero blocks of a token or a weight carry the least scale, 2^-127, wherever they lie; a token of zeros."""
+    say(f"gemm fp8 zero blocks {M} N {N}")
+    w, x = case(M, N, 2)
+    sw, sx = scale_bytes(M, N)
+    for n, blocks in ((0, [0]), (1, [0, 1, 2]), (2, [9]), (N - 1, [4, 8]), (N // 2, range(T))):
+        for b in blocks:
+            x[n, block_of_columns(b)] = 0
+            sx[n, b] = 0
+    for m, b in ((0, 0), (0, 5), (1, 9), (sw.shape[0] - 1, 3)):
+        w[128 * m:128 * m + 128, block_of_columns(b)] = 0
+        sw[m, b] = 0
+    assert np.array_equal(product(w, sw, x, sx), rounded(x @ w.T))
+
+
+@pytest.mark.parametrize("M,N", SIZES)
+def test_least_scales(M, N):
+    """2^-127 on blocks that hold something, beside ordinary ones."""
+    say(f"gemm fp8 least scales {M} N {N}")
+    w, x = case(M, N, 3)
+    which = np.arange(M) % 2
+    for b in range(T):
+        w[:, block_of_columns(b)] *= (which == b % 2)[:, None]
+    sw, sx = scale_bytes(M, N)
+    sx[1::3, 1::2] = 0  # of rows with which == 1: their results are whole numbers times 2^-127
+    sw[:, 1::2] = 137   # 2^10
+    got = product(w, sw, x, sx)
+    wf, xf = scaled(w, sw, x, sx)
+    assert np.array_equal(got, rounded(xf @ wf.T))
