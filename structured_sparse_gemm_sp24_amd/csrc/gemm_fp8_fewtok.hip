@@ -6,8 +6,9 @@
 // ranges. A wave requests U tiles' operands at a time before their products: per lane and row block the 16-byte run
 // of its slot in the value tile and its 32-bit index, per fragment the two 16-byte runs of its token's row that are
 // the operand's halves (k0 + 16 q and k0 + 64 + 16 q), and the scales of the tile. A tile's product starts from
-// zero; then acc = fma(product, 2^(x scale + w scale), acc), the power of two formed once a fragment and tile (NaN
-// where either scale is).
+// zero; then acc = fma(product, 2^(x scale + w scale), acc), the power of two formed once a fragment and tile. (A
+// NaN scale of the weight is noted beside the loop and put into the sums after it: as a factor in the loop, 11008 x 4096 at
+// N = 16 took 12.5 us against 9.2.)
 //
 // Reads go through buffer descriptors: row blocks past M, tokens past N, runs past K (inside a row as well: what
 // follows there may be a NaN code, which a zero weight would not cancel) and tiles past a wave's range read zeros.
@@ -68,6 +69,8 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
 #pragma unroll
         for (int f = 0; f < NF; f++) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    uint32_t most = 0, most2 = 0;  // the largest weight scales: 255 makes the sums NaN after the loop
+
 #pragma unroll 1
     for (int t = t0; t < t1; t += U) {
         i32x4 av[U][R];
@@ -100,10 +103,13 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; u++)
+        for (int u = 0; u < U; u++) {
+            most = max(most, sw[u]);
+            if constexpr (TWO) most2 = max(most2, sw2[u]);
 #pragma unroll
             for (int f = 0; f < NF; f++) {
-                const float x = scale_value(sx[u][f]), s1 = x * scale_value(sw[u]), s2 = TWO ? x * scale_value(sw2[u]) : s1;
+                const float x = scale_value(sx[u][f]), s1 = __builtin_amdgcn_ldexpf(x, (int)sw[u] - 127);
+                const float s2 = TWO ? __builtin_amdgcn_ldexpf(x, (int)sw2[u] - 127) : s1;
 #pragma unroll
                 for (int i = 0; i < R; i++) {
                     const float s = TWO && ((b0 + i) >> 3) != (b0 >> 3) ? s2 : s1;
@@ -112,6 +118,16 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
                     for (int e = 0; e < 4; e++) acc[i][f][e] = fmaf(p[e], s, acc[i][f][e]);
                 }
             }
+        }
+    }
+    if (max(most, most2) == 255u) {
+#pragma unroll
+        for (int i = 0; i < R; i++)
+            if ((TWO && ((b0 + i) >> 3) != (b0 >> 3) ? most2 : most) == 255u)
+#pragma unroll
+                for (int f = 0; f < NF; f++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[i][f][e] = __uint_as_float(0x7FC00000u);
     }
     if (wave > 0) {
 #pragma unroll
