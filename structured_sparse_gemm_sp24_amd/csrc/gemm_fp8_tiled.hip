@@ -66,7 +66,7 @@ struct Args {
     int64_t M, K, N, ldx, lds, ldy;
     int S;  // stages
     int tilesM, tilesN;
-    int y_vec;  // the row pitch allows 8-byte stores
+    int y_vec;  // every row of Y starts on 8 bytes
 };
 
 __device__ __forceinline__ i32x4 make_rsrc(const void* base, int64_t bytes) {
@@ -439,9 +439,16 @@ __device__ __forceinline__ void stage(const Args& a, const Desc& dc, const Desc&
     }
 }
 
+// How a wave stores its outputs: one by one where it crosses M or N, else eight bytes a lane. Where every row of Y starts on
+// eight bytes, non-temporal stores are the faster (28672 x 512 at N = 8192 157 us against 183); elsewhere rows share
+// cache lines between waves, and the caches put them together (28671 x 512 228 us against 430; one by one 384; 11007 x 4096
+// at N = 1500 80, 90 and 100).
+enum { EDGE, EVEN_PITCH, ODD_PITCH };
+typedef u32x2 u32x2_any __attribute__((aligned(2)));  // at any element
+
 // Token-major epilogue from registers: each accumulator is 4 consecutive outputs of token row n. A quad transpose
 // across four row fragments gives each lane quad one token row, so a store instruction covers 16 rows x 64 outputs.
-template <bool F16, bool FULL>
+template <bool F16, int STORE>
 __device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Units& u, const Args& a, int64_t mw,
                                            int64_t nw, int lane) {
     const int q = lane >> 4, r = lane & 15, x = r & 3, c = r >> 2;
@@ -464,8 +471,10 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Uni
             for (int s = 0; s < 4; s++) {
                 const int64_t n = nw + 16 * j + 4 * c + s, m = mw + 64 * ig + 16 * x + 4 * q;
                 uint16_t* const p = Y + n * a.ldy + m;
-                if constexpr (FULL) {
+                if constexpr (STORE == EVEN_PITCH) {
                     __builtin_nontemporal_store(u32x2{v[s][0], v[s][1]}, reinterpret_cast<u32x2*>(p));
+                } else if constexpr (STORE == ODD_PITCH) {
+                    *reinterpret_cast<u32x2_any*>(p) = u32x2{v[s][0], v[s][1]};
                 } else if (n < a.N) {
 #pragma unroll
                     for (int t = 0; t < 4; t++)
@@ -578,8 +587,9 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
         buf ^= 1;
         const int64_t mw = cur.m0 + wm0, nw = cur.n0 + wn0;
         if (__builtin_expect(far_apart(g.u), 0)) apart |= 1ull << ((k - 1) & 63);
-        else if (mw + WM <= a.M && nw + WN <= a.N && a.y_vec) store_tile<F16, true>(acc, g.u, a, mw, nw, lane);
-        else store_tile<F16, false>(acc, g.u, a, mw, nw, lane);
+        else if (mw + WM > a.M || nw + WN > a.N) store_tile<F16, EDGE>(acc, g.u, a, mw, nw, lane);
+        else if (a.y_vec) store_tile<F16, EVEN_PITCH>(acc, g.u, a, mw, nw, lane);
+        else store_tile<F16, ODD_PITCH>(acc, g.u, a, mw, nw, lane);
         if (!next.valid) break;
 #pragma unroll
         for (int i = 0; i < FM; i++)
