@@ -187,14 +187,16 @@ __global__ __launch_bounds__(256) void add_parts_kernel(const float* __restrict_
 
 }  // namespace
 
-// Parts that the tokens are split into: as many as keep the workgroups within one a compute unit of 256, and at least
-// 256 tokens a part (768 x 768 over 6304 tokens, 36 tiles: 27.9 us with 7 parts, 30.8 with 14; 1024 x 4096 over 2048 tokens,
+// Parts that the tokens are split into: as many as keep the workgroups within one a compute unit of 256, at least
+// 256 tokens a part, and none without tokens, a part being whole steps of 128 (768 x 768 over 6304 tokens, 36 tiles: 27.9 us with 7 parts, 30.8 with 14; 1024 x 4096 over 2048 tokens,
 // 256 tiles: 37.7 in one part, 41.2 in two; 2048 x 1024 over 300 tokens: 15.6 in one part, 22.5 in two).
 int grad_weight_parts(int64_t M, int64_t K, int64_t N) {
     const int64_t tiles = ((M + BT - 1) / BT) * ((K + BT - 1) / BT);
     const int64_t want = 256 / tiles, most = N / 256;
     const int64_t p = want < most ? want : most;
-    return (int)(p < 1 ? 1 : p);
+    if (p < 2) return 1;
+    const int64_t steps = (N + 2 * BN - 1) / (2 * BN), per = (steps + p - 1) / p;  // whole steps a part
+    return (int)((steps + per - 1) / per);
 }
 
 // The 256 x 256 kernel (one workgroup a compute unit) where its rounds of the chip are full enough: in one round, where the

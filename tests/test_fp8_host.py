@@ -181,3 +181,15 @@ def test_launch_limits(lib):  # noqa: F811
         assert lib.sp24_grad_weight_fp8_bytes(1 << 22, K, 64, ctypes.byref(n)) == SHAPE
         assert lib.sp24_grad_weight_fp8(*changed(GRAD, N=64, M=1 << 22, lddy=1 << 22, K=K, ldx=K, lds=1 << 13, ldw=K)) == SHAPE
     assert lib.sp24_grad_weight_fp8_bytes(1 << 22, 511 * 256, 64, ctypes.byref(n)) == 0 and n.value == 0
+
+
+@pytest.mark.parametrize("M,K", [(128, 128), (640, 640), (768, 768), (2048, 1024)])
+def test_no_part_without_tokens(lib, M, K):  # noqa: F811
+    """The tokens' parts of the weight's gradient, 128 tokens at a time: as many partial sums as parts that hold some."""
+    n = ctypes.c_int64(-1)
+    for N in (512, 600, 1000, 1300, 2000, 2049, 3000, 5000, 6304, 20000):
+        assert lib.sp24_grad_weight_fp8_bytes(M, K, N, ctypes.byref(n)) == 0 and n.value % (4 * M * K) == 0
+        parts = n.value // (4 * M * K)
+        if parts:
+            steps = -(-N // 128)
+            assert parts > 1 and parts == -(-steps // -(-steps // parts))
