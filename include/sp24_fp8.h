@@ -73,8 +73,9 @@ int sp24_decompress_fp8(const uint8_t* values, const uint8_t* meta, const uint8_
  *   Y[n, m] = sum_b 2^(x_scales[n, b] + w_scales[m / 128, b] - 254) * sum_{kept k in block b} w[m, k] * x[n, k],
  *   sums over blocks in fp32, Y: N x M (pitch ldy >= M) of out_dtype BF16 or FP16 (rounded once; FP16 overflows to
  *   infinity). X codes: N x K, pitch ldx. Inside a block the 8-bit matrix instructions align the 64 products to about
- *   2^-13 of the largest one (measured), far below the codes' own 2^-4 and invisible after rounding to 16 bits; an
- *   FP32 result would promise more than that, so none is offered.
+ *   2^-13 of the largest one (measured): far below the codes' own 2^-4, and by norm below the rounding to 16 bits, but a
+ *   single result whose products cancel can be off by more than that rounding. An FP32 result would promise more, so
+ *   none is offered.
  * A NaN scale of x makes its token's row NaN, one of the weight its 128 output channels. The product of two scales
  * must be below 2^128; one below 2^-149 may count as zero. Results depend on the sizes, which choose the kernel, only
  * through the order of the fp32 sums, however far apart a token's scales are. */

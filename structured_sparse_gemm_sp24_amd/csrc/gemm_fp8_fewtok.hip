@@ -14,8 +14,9 @@
 // follows there may be a NaN code, which a zero weight would not cancel) and tiles past a wave's range read zeros.
 // The waves' sums are added through LDS in wave order.
 //
-// The weight's bytes bound it where there are enough of them: 28672 x 8192 at one token 29.4 us, 5.0 TB/s, 11008 x 4096 8.7
-// us, 3.2 TB/s; a 10 MB weight (4096 x 4096, 3.9 us) is a launch and two trips to memory.
+// The weight's bytes bound it where there are enough of them: 28672 x 8192 at one token 28.9 us, 5.1 TB/s, 11008 x 4096 8.3
+// us, 3.4 TB/s; a 10 MB weight (4096 x 4096, 4.7 us; 4.0 where the weight is in the Infinity Cache) is a launch and two
+// trips to memory.
 #include "fp8_device.h"
 #include "sp24_launch.h"
 
@@ -187,21 +188,21 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
 // Infinity Cache (us):
 //  R is the least of 1, 2 and 3 that leaves at most one workgroup a compute unit, and 4 (8 with one fragment) beyond; the
 //  fewer, the more often each workgroup's X is read again, and at most 8 tokens are too few for that to count:
-//  one fragment: 4096 x 4096 (256 row blocks) at N = 1 / 8 / 16 4.4 / 5.0 / 5.9 with R = 1; 8192 x 8192 (512) at N = 1 / 8
-//    9.8 / 11.9 with R = 1, 10.9 / 11.3 with 2, at N = 16 11.8 with R = 2 against 15.4 with 1; 11008 x 4096 (688) at N = 1 / 8
-//    8.7 / 9.0 with R = 2 against 8.5 / 10.4 with 1, at N = 16 9.3 with R = 3 against 10.0 with 4; 14336 x 4096 (896) at N =
-//    16 10.8 with R = 4 against 12.7 with 3; 28672 x 8192 (1792) at N = 1 / 8 29.4 / 31.1 with R = 2, at N = 16 33.0 with R
-//    = 8 against 35.5 with 4;
-//  two: 4096 x 4096 8.4 with R = 1 against 9.2 with 2, 8192 x 8192 15.9 with 2 against 24.8 with 1, 11008 x 4096 11.7 with 3
-//    against 12.1 with 4, 28672 x 8192 37.8 with 4 against 53.8 with 2;
-//  three: 4096 x 4096 10.3 with R = 1 against 11.5 with 2, 8192 x 8192 20.8 with 2 against 31.9 with 1, 11008 x 4096 13.7
-//    with 3 against 14.4 with 4, 28672 x 8192 40.9 with 4 against 51.5 with 3;
-//  four, and groups of 64 tokens: 4096 x 4096 at N = 64 14.4 with R = 1 against 16.8 with 4, at N = 100 15.4 with 2, at N =
-//    190 17.2 with 4 against 26.8 with 3 (258 workgroups); 11008 x 4096 at N = 64 17.1 with 3 against 18.1 with 4.
+//  one fragment: 4096 x 4096 (256 row blocks) at N = 1 / 8 / 16 4.8 / 5.1 / 6.1 with R = 1; 8192 x 8192 (512) at N = 1 / 8
+//    9.8 / 11.9 with R = 1, 11.8 / 11.7 with 2, at N = 16 12.1 with R = 2 against 15.5 with 1; 11008 x 4096 (688) at N = 1 / 8
+//    8.2 / 8.8 with R = 2 against 8.1 / 9.5 with 1, at N = 16 9.3 with R = 3 against 10.9 with 4; 14336 x 4096 (896) at N =
+//    16 11.9 with R = 4 against 12.8 with 3; 28672 x 8192 (1792) at N = 1 / 8 28.6 / 30.0 with R = 2 against 27.7 / 35.9 with
+//    1, at N = 16 31.5 with R = 8 against 36.5 with 4;
+//  two (N = 32): 4096 x 4096 8.8 with R = 1 against 9.5 with 2, 8192 x 8192 16.5 with 2 against 25.8 with 1, 11008 x 4096
+//    12.5 with 3 and with 4 alike, 28672 x 8192 37.0 with 4 against 46.5 with 3;
+//  three (N = 40; 37 the last two): 4096 x 4096 10.3 with R = 1 against 11.5 with 2, 8192 x 8192 19.8 with 2 against 32.2
+//    with 1, 11008 x 4096 13.2 with 3 against 14.3 with 4, 28672 x 8192 41.2 with 4 against 51.4 with 3;
+//  four, and groups of 64 tokens: 4096 x 4096 at N = 64 14.5 with R = 1 against 17.9 with 4, at N = 100 15.3 with 2, at N =
+//    190 18.2 with 4 against 26.9 with 3 (258 workgroups); 11008 x 4096 at N = 64 17.3 with 3 against 19.1 with 4.
 // The groups stream the weight once each, from L2 after the first; the tiled kernel reads it once but fills the chip
 // only with many tiles. Up to 2.25 workgroups of 64 x 64 a compute unit this one is the faster (4096 x 4096 at N = 512, 2:
-// 28.9 against 37 us; 11008 x 4096 at N = 200, 2.7: 40.7 against 38.8; 28672 x 8192 at N = 64, 1.75: 56 against 71, at N =
-// 100, 3.5: 89 against 75).
+// 29.6 against 34.3 us; 11008 x 4096 at N = 200, 2.7: 41.7 against 35.4; 28672 x 8192 at N = 64, 1.75: 56.3 against 64.9, at
+// N = 100, 3.5: 88.4 against 70.3).
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s) {
     const int64_t nb = (g.M + 15) / 16, groups = (g.N + 63) / 64, cus = device_cus();
     if (4 * ((nb + 3) / 4) * groups > 9 * cus && g.N > 64) return launch_gemm_fp8_tiled(g, s);

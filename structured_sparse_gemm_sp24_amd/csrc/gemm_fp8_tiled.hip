@@ -25,11 +25,14 @@
 //
 // The scales themselves are fetched eight stages at a time, a word each, into a buffer of their own.
 //
-// 28672 x 8192 on 8192 tokens: 1344 to 1380 us, 2.8 dense-equivalent PFLOP/s. What bounds it is a SIMD's issue: for each
-// matrix instruction of 16 cycles it issues about seven others of four, the four multiplications among them, for the
-// most part not beside the other wave's matrix instructions, since the stage's barrier keeps the eight waves in step.
-// Matrix cores are busy 31 % of the cycles at the 2.0 GHz that the chip holds under this load. HBM is not near: 2.1 GB
-// fetched a call, 1.5 TB/s.
+// 28672 x 8192 on 8192 tokens: 1308 to 1339 us (medians of 60 calls in a row; the first ten after a pause take 1410), 2.9
+// dense-equivalent PFLOP/s. What bounds it is a SIMD's issue: for each matrix instruction of 16 cycles it issues 6.5 others
+// of four, the four multiplications among them, for the most part not beside the other wave's matrix instructions, since the
+// stage's barrier keeps the eight waves in step: matrix cores are busy 32 % of the cycles at the 2.0 GHz that the chip holds
+// under this load. Those instructions account for 42 cycles a matrix instruction if nothing overlaps; the 50 that the
+// counters show leave the rest to the waits at the barrier. HBM is not near: 2.1 GB fetched a call, 1.6 TB/s.
+//
+// Summing a tile again costs fourteen times the tile: 11008 x 4096 at N = 1500 1100 us where every tile is, against 77.
 //
 // Persistent: a workgroup walks its tiles (neighbouring tiles on the same XCD at the same time, groups of 8
 // tile-rows) with the LDS pipeline continued across tiles.
@@ -50,7 +53,7 @@ struct Cfg {
     static constexpr int BN = BN_, WAVES = BN_ / 32;
     // whether a stage's loads are spread over the matrix instructions after the barrier (28672 x 8192 x 8192:
     // 1379 us against 1414 us in one burst) or issued at once (128 wide, two workgroups a compute unit: 11008 x 4096 at
-    // N = 512 35.5 us against 40 us spread)
+    // N = 512 35.5 us against 40 us spread), both before the scales' tracking was shortened
     static constexpr bool SPREAD = BN == 256;
     static constexpr int STAGE_BYTES = A_BYTES + META_BYTES + BN * BK;
     static constexpr int CHUNK_BYTES = BN * CHUNK * 4;  // a word for each scale
@@ -632,11 +635,12 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
 
 // Tile width by the rounds of the chip that the tiles take: one 256-wide tile a compute unit, or two 128-wide ones. A round
 // of 256-wide tiles is the faster where it is full enough that the 128-wide tiles (half as many columns each) would
-// need their last round's second half as well, and always from four rounds on. Measured (us, 128 wide / 256 wide;
-// tiles of 256 x 256): 11008 x 4096 at N = 512 (86) 37.7 / 51.3, 700 (129) 57.9 / 56.2, 1024 (172) 62.2 / 56.3, 1500 (258)
-// 83.4 / 101.9, 2048 (344) 91.2 / 102.7, 2304 (387) 123.3 / 112.3, 3100 (559) 137.1 / 149.6, 4608 (774) 199.4 / 195.5,
-// 6100 (1032) 251.1 / 241.3; 4096 x 4096 at N = 4096 (256) 74.5 / 68.3; 8192 x 8192 at N = 1024 (128) 76.0 / 94.2, 1100 (160)
-// 110.3 / 95.7; 6304 x 768 at N = 6304 (625) 45.2 / 53.7; 28672 x 8192 at N = 8192 (3584) 1588 / 1378.
+// need their last round's second half as well, and from four rounds on, where the two are near each other until the weight no
+// longer fits the caches. Measured (us, 128 wide / 256 wide;
+// tiles of 256 x 256): 11008 x 4096 at N = 512 (86) 35.6 / 49.5, 700 (129) 56.6 / 58.2, 1024 (172) 57.1 / 52.9, 1500 (258)
+// 81.0 / 99.9, 2048 (344) 88.7 / 99.7, 2304 (387) 110.0 / 100.2, 3100 (559) 136.7 / 147.1, 4608 (774) 188.8 / 193.9,
+// 6100 (1032) 243.6 / 244.1; 4096 x 4096 at N = 4096 (256) 60.4 / 56.7; 8192 x 8192 at N = 1024 (128) 69.3 / 92.6, 1100 (160)
+// 101.3 / 94.0; 6304 x 768 at N = 6304 (625) 43.6 / 52.4; 28672 x 8192 at N = 8192 (3584) 1515 / 1328.
 hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s) {
     const int64_t cus = device_cus(), m = (g.M + BM - 1) / BM, wide = m * ((g.N + 255) / 256), narrow = m * ((g.N + 127) / 128);
     const int64_t rounds = (wide + cus - 1) / cus;

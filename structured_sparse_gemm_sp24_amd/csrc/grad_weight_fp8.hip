@@ -15,7 +15,7 @@
 // Where the weight has too few tiles for the chip, the tokens are split; each part writes fp32 sums to
 // the workspace, and a second kernel adds the parts in order.
 //
-// 768 x 768 over 6304 tokens (7 parts): 19.7 us and 4.9 for the sums. Its matrix instructions are 3.5 us; each of the 252
+// 768 x 768 over 6304 tokens (7 parts): 20.2 us and 4.2 for the sums. Its matrix instructions are 3.5 us; each of the 252
 // workgroups reads its 24 KB a stage through its XCD's L2, 78 MB fetched in all for 14.5 MB of operands, at 3.9 TB/s,
 // and writes 16.5 MB of partial sums. Stages of 32 tokens took 29.6 us in all against 27.9, 14 parts 30.8 us.
 #include "fp8_device.h"

@@ -1,8 +1,9 @@
 // Gradient of the weight from the 8-bit copy of the input, for weights with tiles enough for the chip (the formulas and
 // the operands' layout are in grad_weight_fp8.hip): workgroup tile 256 (k) x 256 (m), eight waves of 128 x 64, two a
 // SIMD, 8 x 4 fragments of v_mfma_f32_16x16x32_bf16 (128 sums a lane). While one wave of a SIMD converts codes, reads
-// fragments or stores, the other's matrix instructions run: 11008 x 4096 over 4096 tokens 338 us (1.09 PFLOP/s), 8192^3
-// 917 us (1.20), against 382 and 1037 us with four waves of 128 x 128, which read a quarter less LDS; v_mfma_f32_32x32x16_bf16
+// fragments or stores, the other's matrix instructions run: 11008 x 4096 over 4096 tokens 338 us (1.09 PFLOP/s) on one
+// set of inputs, 357 to 365 us on three in turn; 8192^3 917 us (1.20), against 382 and 1037 us (on one set) with four waves
+// of 128 x 128, which read a quarter less LDS; v_mfma_f32_32x32x16_bf16
 // was slower. Matrix cores are busy 42 % of the cycles at 2.15 GHz; what bounds it is the conversion and LDS traffic beside them
 // (every code is written to LDS as bf16 and read back transposed) and the last, part-full round of tiles.
 //
