@@ -150,3 +150,28 @@ def test_least_scales(M, N):
     got = product(w, sw, x, sx)
     wf, xf = scaled(w, sw, x, sx)
     assert np.array_equal(got, rounded(xf @ wf.T))
+
+
+def test_far_apart_among_many_tiles():
+    """More than 64 tiles a wave, of which some are summed again."""
+    M, N, k = 4096, 280000, 272
+    say(f"gemm fp8 far scales among many tiles {M}x{k} N {N}")
+    rng = np.random.default_rng(5)
+    w = rng.integers(-3, 4, (M, k)).astype(np.float64)
+    w *= ref.keep2(w)
+    w[::2, 128:256] = 0
+    x = rng.integers(-4, 5, (N, k)).astype(np.float32)
+    sx = np.full((N, 3), 127)
+    far = np.arange(N) % 20011 == 7
+    sx[far, 1] = 227
+    sw = np.full((M // 128, 3), 127)
+    v, m, s = sp.sp24_prune_compress_fp8(torch.from_numpy(w).float().cuda())
+    unit = s.float().repeat_interleave(8, 0).unsqueeze(2).expand(-1, -1, 1024).reshape(-1)
+    codes = torch.from_numpy(x).cuda().to(torch.float8_e4m3fn)
+    y = sp.sp24_gemm_fp8((v.float() * unit).to(torch.float8_e4m3fn), m, e8m0(sw), M, codes, e8m0(sx))
+    at = np.unique(np.concatenate([np.flatnonzero(far), np.flatnonzero(far) + 1, rng.integers(0, N, 500)]))
+    got = ref.f64(y[torch.from_numpy(at).cuda()])
+    big = np.repeat(2.0 ** (sx[at].astype(np.float64) - 127), 128, 1)[:, :k] * x[at]
+    want = big @ w.T
+    assert np.array_equal(got[:, ::2], rounded(want)[:, ::2])
+    assert (np.abs(got - want) <= 1.01 * ref.UB * np.abs(want) + 20 * ref.U32 * (np.abs(big) @ np.abs(w).T)).all()
