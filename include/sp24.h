@@ -97,8 +97,9 @@ typedef enum { SP24_SCORE_MAGNITUDE = 0, SP24_SCORE_WANDA = 1 } sp24_score;
  *                      Y is N x M; row pitches ldx >= K and ldy >= M. */
 typedef enum { SP24_FEATURE_MAJOR = 0, SP24_TOKEN_MAJOR = 1 } sp24_layout;
 
-/* Activation of the fused int8 epilogue: none, or GELU(y) = y/2 (1 + erf(y / sqrt 2)). */
-typedef enum { SP24_ACT_NONE = 0, SP24_ACT_GELU = 1 } sp24_activation;
+/* Activation of a fused epilogue: none, GELU(y) = y/2 (1 + erf(y / sqrt 2)), ReLU(y) = max(y, 0), SiLU(y) = y / (1 + e^-y).
+ * The int8 epilogue takes the first two; all four: sp24_layer.h. */
+typedef enum { SP24_ACT_NONE = 0, SP24_ACT_GELU = 1, SP24_ACT_RELU = 2, SP24_ACT_SILU = 3 } sp24_activation;
 
 /* Per-input-channel activation norms for Wanda scoring (zyxy.net Wanda lecture, section 2.1).
  *   norms[j] = sqrt( sum_{n<N} X[j*ldx + n]^2 ),  j < K.

@@ -1,8 +1,8 @@
 """sp24: 2:4 structured-sparse prune/compress and sparse GEMM for AMD MI355X (gfx950).
 
-Thin Python binding over the C ABI of ``libsp24.so`` (declared in include/sp24.h, and include/sp24_fp8.h for
-the 8-bit floating-point operators, whose functions live in fp8.py and are exported here): the functions
-below have the C entry points' names and only marshal arguments -- torch tensors supply device
+Thin Python binding over the C ABI of ``libsp24.so`` (declared in include/sp24.h, include/sp24_fp8.h for the 8-bit
+floating-point operators and include/sp24_layer.h for what surrounds a Linear layer's product, whose functions live in fp8.py
+and layer.py and are exported here): the functions below have the C entry points' names and only marshal arguments -- torch tensors supply device
 memory and the current HIP stream; every step runs in the library's HIP kernels. If the library is
 not built, or the device is not gfx950, the calls raise; there is no CPU fallback.
 """
@@ -21,7 +21,7 @@ SP24_ERR_DTYPE, SP24_ERR_ARG, SP24_ERR_DEVICE, SP24_ERR_HIP = -4, -5, -6, -7
 SP24_BF16, SP24_FP16, SP24_FP32, SP24_I8, SP24_I32, SP24_FP8 = 0, 1, 2, 3, 4, 5
 SP24_SCORE_MAGNITUDE, SP24_SCORE_WANDA = 0, 1
 SP24_FEATURE_MAJOR, SP24_TOKEN_MAJOR = 0, 1
-SP24_ACT_NONE, SP24_ACT_GELU = 0, 1
+SP24_ACT_NONE, SP24_ACT_GELU, SP24_ACT_RELU, SP24_ACT_SILU = 0, 1, 2, 3
 
 # every symbol the headers in include/ declare
 EXPORTS = ("sp24_col_norms", "sp24_compressed_bytes", "sp24_prune_compress", "sp24_prune_mask",
@@ -33,6 +33,8 @@ EXPORTS = ("sp24_col_norms", "sp24_compressed_bytes", "sp24_prune_compress", "sp
            "sp24_quant_fp8", "sp24_rmsnorm_fp8", "sp24_rmsnorm_backward_bytes", "sp24_rmsnorm_backward",
            "sp24_prune_compress_fp8", "sp24_decompress_fp8", "sp24_gemm_fp8",
            "sp24_grad_weight_fp8_bytes", "sp24_grad_weight_fp8",
+           "sp24_gemm_bf16_fused", "sp24_gemm_fp8_fused", "sp24_epilogue_backward_bytes", "sp24_epilogue_backward",
+           "sp24_adamw",
            "sp24_status_string")
 
 _TORCH_TO_SP24 = {torch.bfloat16: SP24_BF16, torch.float16: SP24_FP16, torch.float32: SP24_FP32,
@@ -78,6 +80,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sp24_bench_stream_read_blocks.argtypes = [I64, ctypes.POINTER(I64)]
     lib.sp24_bench_stream_read.argtypes = [P, I64, P, P]
     fp8.bind(lib)
+    layer.bind(lib)
     for fn in EXPORTS[:-1]:
         getattr(lib, fn).restype = I
     lib.sp24_status_string.argtypes = [I]
@@ -399,6 +402,8 @@ def sp24_bench_stream_read(src: torch.Tensor, nbytes: int | None = None, sink: t
     return sink
 
 
-from . import fp8  # noqa: E402  (needs the names above)
+from . import fp8, layer  # noqa: E402  (need the names above)
 from .fp8 import (sp24_decompress_fp8, sp24_gemm_fp8, sp24_grad_weight_fp8, sp24_prune_compress_fp8,  # noqa: E402,F401
                   sp24_quant_fp8, sp24_rmsnorm_backward, sp24_rmsnorm_fp8)
+from .layer import (sp24_adamw, sp24_adamw_state, sp24_epilogue_backward, sp24_gemm_bf16_fused,  # noqa: E402,F401
+                    sp24_gemm_fp8_fused)

@@ -2,6 +2,7 @@
 // check, and the launches. Declarations and the contract live in include/sp24_fp8.h.
 #include "../../include/sp24.h"
 #include "../../include/sp24_fp8.h"
+#include "../../include/sp24_layer.h"
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -40,6 +41,25 @@ int hip_status(hipError_t e) { return e == hipSuccess ? SP24_OK : SP24_ERR_HIP; 
         const int st_ = (call);         \
         if (st_ != SP24_OK) return st_; \
     } while (0)
+
+// The product's operands and output, put into g.
+int check_gemm(const uint8_t* values, const uint8_t* meta, const uint8_t* w_scales, int64_t M, int64_t K, const uint8_t* X, int64_t N,
+               int64_t ldx, const uint8_t* x_scales, int64_t lds, void* Y, int out_dtype, int64_t ldy, sp24::Fp8GemmArgs& g) {
+    if (!values || !meta || !w_scales || !X || !x_scales || !Y) return SP24_ERR_NULL;
+    if (out_dtype != SP24_BF16 && out_dtype != SP24_FP16) return SP24_ERR_DTYPE;
+    SP24_TRY(check_nk(N, K, kMaxK));
+    if (M < 1 || M > kMaxWeightRows) return SP24_ERR_SHAPE;
+    // tiles of 256 x 128 with 256 threads or of 256 x 256 with 512: one workgroup each where K is a single block
+    if (((M + 255) / 256) * blocks_of(N) > kMaxGrid || tiles_256(M, N) > kMaxGrid / 2) return SP24_ERR_SHAPE;
+    SP24_TRY(check_matrix(X, K, ldx, 1));
+    SP24_TRY(check_scales(K, lds));
+    if (ldy < M || ldy >= kMaxPitch) return SP24_ERR_SHAPE;
+    if (!aligned16(values) || !aligned16(meta) || !aligned16(Y)) return SP24_ERR_ALIGN;
+    g.values = values; g.meta = meta; g.ws = w_scales; g.X = X; g.xs = x_scales; g.Y = Y;
+    g.M = M; g.K = K; g.N = N; g.ldx = ldx; g.lds = lds; g.ldy = ldy;
+    g.out_fp16 = out_dtype == SP24_FP16;
+    return SP24_OK;
+}
 
 }  // namespace
 
@@ -136,21 +156,26 @@ int sp24_decompress_fp8(const uint8_t* values, const uint8_t* meta, const uint8_
 int sp24_gemm_fp8(const uint8_t* values, const uint8_t* meta, const uint8_t* w_scales, int64_t M, int64_t K,
                   const uint8_t* X, int64_t N, int64_t ldx, const uint8_t* x_scales, int64_t lds, void* Y, int out_dtype,
                   int64_t ldy, void* stream) {
-    if (!values || !meta || !w_scales || !X || !x_scales || !Y) return SP24_ERR_NULL;
-    if (out_dtype != SP24_BF16 && out_dtype != SP24_FP16) return SP24_ERR_DTYPE;
-    SP24_TRY(check_nk(N, K, kMaxK));
-    if (M < 1 || M > kMaxWeightRows) return SP24_ERR_SHAPE;
-    // tiles of 256 x 128 with 256 threads or of 256 x 256 with 512: one workgroup each where K is a single block
-    if (((M + 255) / 256) * blocks_of(N) > kMaxGrid || tiles_256(M, N) > kMaxGrid / 2) return SP24_ERR_SHAPE;
-    SP24_TRY(check_matrix(X, K, ldx, 1));
-    SP24_TRY(check_scales(K, lds));
-    if (ldy < M || ldy >= kMaxPitch) return SP24_ERR_SHAPE;
-    if (!aligned16(values) || !aligned16(meta) || !aligned16(Y)) return SP24_ERR_ALIGN;
-    SP24_TRY(sp24::check_device());
     sp24::Fp8GemmArgs g;
-    g.values = values; g.meta = meta; g.ws = w_scales; g.X = X; g.xs = x_scales; g.Y = Y;
-    g.M = M; g.K = K; g.N = N; g.ldx = ldx; g.lds = lds; g.ldy = ldy;
-    g.out_fp16 = out_dtype == SP24_FP16;
+    SP24_TRY(check_gemm(values, meta, w_scales, M, K, X, N, ldx, x_scales, lds, Y, out_dtype, ldy, g));
+    SP24_TRY(sp24::check_device());
+    return hip_status(sp24::launch_gemm_fp8(g, static_cast<hipStream_t>(stream)));
+}
+
+int sp24_gemm_fp8_fused(const uint8_t* values, const uint8_t* meta, const uint8_t* w_scales, int64_t M, int64_t K,
+                        const uint8_t* X, int64_t N, int64_t ldx, const uint8_t* x_scales, int64_t lds, const float* bias,
+                        int activation, const void* R, int64_t ldr, void* Z, int64_t ldz, void* Y, int out_dtype, int64_t ldy,
+                        void* stream) {
+    sp24::Fp8GemmArgs g;
+    SP24_TRY(check_gemm(values, meta, w_scales, M, K, X, N, ldx, x_scales, lds, Y, out_dtype, ldy, g));
+    SP24_TRY(sp24::check_epilogue(bias, activation, R, ldr, Z, ldz, Y, ldy, M));
+    if ((R && ldr >= kMaxPitch) || (Z && ldz >= kMaxPitch)) return SP24_ERR_SHAPE;
+    g.epi.on = true;
+    g.epi.act = activation;
+    g.epi.bias = bias;
+    g.epi.R = R, g.epi.ldr = ldr;
+    g.epi.Z = Z, g.epi.ldz = ldz;
+    SP24_TRY(sp24::check_device());
     return hip_status(sp24::launch_gemm_fp8(g, static_cast<hipStream_t>(stream)));
 }
 

@@ -20,8 +20,7 @@
 // row pitch. It serves the cases the others do not take: the few-token kernel (gemm_bf16_skinny.hip,
 // N <= 64) and the LDS-tiled kernel (gemm_bf16_tiled.hip, N > 64), each within its alignment and
 // size conditions.
-#include "sp24_device.h"
-#include "sp24_launch.h"
+#include "epilogue.h"
 
 namespace sp24 {
 
@@ -35,7 +34,8 @@ struct DirectArgs {
     int64_t sxk, sxn, sxb;
     void* Y;
     int64_t sym, syn, syb;
-    int out_fp32;
+    int out_fp32, tm;
+    Epilogue epi;
 };
 
 template <int NF>
@@ -90,6 +90,11 @@ __global__ __launch_bounds__(256) void gemm_bf16_direct(DirectArgs d) {
         for (int i = 0; i < 4; i++) {
             const int64_t m = m0 + 4 * q + i;
             if (m >= d.M) continue;
+            if (d.epi.on) {
+                finish1(d.epi, places(d.epi, Y, d.tm ? d.syn : d.sym, d.out_fp32, blockIdx.z), d.out_fp32 ? T_FP32 : T_BF16, acc[f][i],
+                        d.epi.bias ? d.epi.bias[m] : 0.f, d.tm ? n : m, d.tm ? m : n);
+                continue;
+            }
             const int64_t o = m * d.sym + n * d.syn;
             if (d.out_fp32)
                 reinterpret_cast<float*>(Y)[o] = acc[f][i];
@@ -113,6 +118,8 @@ static hipError_t launch_gemm_bf16_direct(const GemmArgs& g, hipStream_t s) {
     d.syn = g.tm ? g.ldy : 1;
     d.syb = g.sy;
     d.out_fp32 = g.out_fp32;
+    d.tm = g.tm;
+    d.epi = g.epi;
     const unsigned gy = (unsigned)((g.M + 63) / 64);
     // grid z covers at most 65535 batch entries per launch
     for (int64_t b0 = 0; b0 < g.batch; b0 += 65535) {
@@ -120,6 +127,7 @@ static hipError_t launch_gemm_bf16_direct(const GemmArgs& g, hipStream_t s) {
         DirectArgs e = d;
         e.X = d.X + b0 * d.sxb;
         e.Y = static_cast<char*>(d.Y) + b0 * d.syb * (g.out_fp32 ? 4 : 2);
+        e.epi = entries_from(d.epi, b0, g.out_fp32);
         if (g.N <= 16)
             hipLaunchKernelGGL(gemm_bf16_direct<1>, dim3((unsigned)((g.N + 15) / 16), gy, gz), dim3(256), 0, s, e);
         else

@@ -22,8 +22,7 @@
 //  - at the end the S partial 16 x 16 accumulators are summed through LDS in wave order
 //    (deterministic), rounded if the output is bf16, and stored into Y (N x M) with bounds checks.
 // A batch of products sharing the weight is grid dimension y.
-#include "sp24_device.h"
-#include "sp24_launch.h"
+#include "epilogue.h"
 
 namespace sp24 {
 namespace fewtok {
@@ -37,6 +36,7 @@ struct Args {
     void* Y;
     int64_t ldy, syb;
     int out_fp32;
+    Epilogue epi;
 };
 
 constexpr uint32_t RSRC_FLAGS = 0x00020000u;
@@ -194,7 +194,9 @@ __global__ __launch_bounds__(64 * S) void gemm_bf16_fewtok(Args g) {
         const int64_t m = b * 16 + row;
         if (m < M && col < N) {
             const int64_t o = (int64_t)col * g.ldy + m;
-            if (g.out_fp32)
+            if (g.epi.on)
+                finish1(g.epi, places(g.epi, Y, g.ldy, g.out_fp32, blockIdx.y), g.out_fp32 ? T_FP32 : T_BF16, s, g.epi.bias ? g.epi.bias[m] : 0.f, col, m);
+            else if (g.out_fp32)
                 reinterpret_cast<float*>(Y)[o] = s;
             else
                 reinterpret_cast<uint16_t*>(Y)[o] = f32_to_bf16_rne(s);
@@ -213,12 +215,14 @@ hipError_t launch(const GemmArgs& g, hipStream_t s) {
     a.Y = g.Y;
     a.ldy = g.ldy; a.syb = g.sy;
     a.out_fp32 = g.out_fp32;
+    a.epi = g.epi;
     const unsigned grid = (unsigned)((g.M + 15) / 16);
     for (int64_t b0 = 0; b0 < g.batch; b0 += 65535) {
         const unsigned gb = (unsigned)(g.batch - b0 < 65535 ? g.batch - b0 : 65535);
         Args e = a;
         e.X = a.X + b0 * a.sxb;
         e.Y = static_cast<char*>(a.Y) + b0 * a.syb * (g.out_fp32 ? 4 : 2);
+        e.epi = entries_from(a.epi, b0, g.out_fp32);
         hipLaunchKernelGGL((gemm_bf16_fewtok<S, D, XR>), dim3(grid, gb), dim3(64 * S), 0, s, e);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;

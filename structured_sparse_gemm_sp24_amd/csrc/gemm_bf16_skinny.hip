@@ -20,8 +20,7 @@
 //    (deterministic), rounded if the output is bf16, and stored with bounds checks (M x N or, token-
 //    major, N x M).
 // A batch of independent products sharing the weight (1x1 conv over B images) is grid dimension y.
-#include "sp24_device.h"
-#include "sp24_launch.h"
+#include "epilogue.h"
 
 namespace sp24 {
 namespace skinny {
@@ -35,6 +34,7 @@ struct Args {
     void* Y;
     int64_t ldy, syb;
     int out_fp32;
+    Epilogue epi;
 };
 
 // X fragment for columns 16 f .. 16 f + 15 of tile k0 (smfmac B operand: lane n = r holds
@@ -276,7 +276,9 @@ __global__ __launch_bounds__(64 * S) void gemm_bf16_skinny(Args g) {
         const int64_t m = (b0 + j) * 16 + row, n = 16 * f + col;
         if (j < nb && m < M && n < N) {
             const int64_t o = TM ? n * ldy + m : m * ldy + n;
-            if (out_fp32)
+            if (g.epi.on)
+                finish1(g.epi, places(g.epi, Y, ldy, out_fp32, blockIdx.y), out_fp32 ? T_FP32 : T_BF16, s, g.epi.bias ? g.epi.bias[m] : 0.f, TM ? n : m, TM ? m : n);
+            else if (out_fp32)
                 reinterpret_cast<float*>(Y)[o] = s;
             else
                 reinterpret_cast<uint16_t*>(Y)[o] = f32_to_bf16_rne(s);
@@ -295,6 +297,7 @@ hipError_t launch(const GemmArgs& g, hipStream_t s) {
     a.Y = g.Y;
     a.ldy = g.ldy; a.syb = g.sy;
     a.out_fp32 = g.out_fp32;
+    a.epi = g.epi;
     const unsigned grid = (unsigned)(((g.M + 15) / 16 + R - 1) / R);
     // grid y covers at most 65535 batch entries per launch
     for (int64_t b0 = 0; b0 < g.batch; b0 += 65535) {
@@ -302,6 +305,7 @@ hipError_t launch(const GemmArgs& g, hipStream_t s) {
         Args e = a;
         e.X = a.X + b0 * a.sxb;
         e.Y = static_cast<char*>(a.Y) + b0 * a.syb * (g.out_fp32 ? 4 : 2);
+        e.epi = entries_from(a.epi, b0, g.out_fp32);
         const dim3 grd(grid, gb), blk(64 * S);
         if (g.tm) {
             if (g.ldx % 8 == 0)

@@ -17,8 +17,7 @@
 // The weight's bytes bound it where there are enough of them: 28672 x 8192 at one token 28.9 us, 5.1 TB/s, 11008 x 4096 8.3
 // us, 3.4 TB/s; a 10 MB weight (4096 x 4096, 4.7 us; 4.0 where the weight is in the Infinity Cache) is a launch and two
 // trips to memory.
-#include "fp8_device.h"
-#include "sp24_launch.h"
+#include "epilogue.h"
 
 namespace sp24 {
 namespace {
@@ -31,6 +30,7 @@ struct Args {
     void* Y;
     int64_t M, K, N, ldx, lds, ldy;
     int y_vec;
+    Epilogue epi;
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
@@ -155,6 +155,13 @@ __global__ __launch_bounds__(64 * S) void gemm_fp8_fewtok_kernel(Args a) {
             const int64_t n = n0 + 16 * f + r;
             if (n >= a.N) continue;
             const f32x4 y = acc[i][f];
+            if (a.epi.on) {
+                const Places at = places(a.epi, static_cast<char*>(a.Y), a.ldy, false, 0);
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (m0 + e < a.M) finish1(a.epi, at, F16 ? T_FP16 : T_BF16, y[e], a.epi.bias ? a.epi.bias[m0 + e] : 0.f, n, m0 + e);
+                continue;
+            }
             uint16_t* const p = static_cast<uint16_t*>(a.Y) + n * a.ldy + m0;
             const u32x2 w = u32x2{pack16<F16>(y[0], y[1]), pack16<F16>(y[2], y[3])};
             if (a.y_vec && m0 + 3 < a.M) {
@@ -174,6 +181,7 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
     a.values = g.values; a.meta = g.meta; a.ws = g.ws; a.X = g.X; a.xs = g.xs; a.Y = g.Y;
     a.M = g.M; a.K = g.K; a.N = g.N; a.ldx = g.ldx; a.lds = g.lds; a.ldy = g.ldy;
     a.y_vec = g.ldy % 4 == 0;  // Y is 16-byte aligned
+    a.epi = g.epi;
     const dim3 grid((unsigned)(((g.M + 15) / 16 + R - 1) / R), (unsigned)((g.N + 16 * NF - 1) / (16 * NF)));
     if (g.out_fp16)
         hipLaunchKernelGGL((gemm_fp8_fewtok_kernel<NF, R, U, S, true>), grid, dim3(64 * S), 0, s, a);

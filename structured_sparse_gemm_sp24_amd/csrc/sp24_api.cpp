@@ -2,6 +2,7 @@
 // and dispatch to the kernels. Declarations and the contract live in include/sp24.h.
 #include "../../include/sp24.h"
 #include "../../include/sp24_bench.h"
+#include "../../include/sp24_layer.h"
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -278,6 +279,38 @@ int sp24_gemm_bf16_ex(const void* values, const uint8_t* meta, int64_t M, int64_
 int sp24_gemm_bf16(const void* values, const uint8_t* meta, int64_t M, int64_t K, const void* X, int64_t N,
                    int64_t ldx, void* Y, int out_dtype, int64_t ldy, void* stream) {
     return sp24_gemm_bf16_ex(values, meta, M, K, X, N, ldx, 0, Y, out_dtype, ldy, 0, 1, SP24_FEATURE_MAJOR, stream);
+}
+
+int sp24_gemm_bf16_fused(const void* values, const uint8_t* meta, int64_t M, int64_t K, const void* X, int64_t N, int64_t ldx,
+                         int64_t x_batch_stride, const float* bias, int activation, const void* R, int64_t ldr,
+                         int64_t r_batch_stride, void* Z, int64_t ldz, int64_t z_batch_stride, void* Y, int out_dtype,
+                         int64_t ldy, int64_t y_batch_stride, int64_t batch, int layout, void* stream) {
+    if (out_dtype != SP24_FP32 && out_dtype != SP24_BF16) {
+        if (!values || !meta || !X || !Y) return SP24_ERR_NULL;
+        return SP24_ERR_DTYPE;
+    }
+    const int es = out_dtype == SP24_FP32 ? 4 : 2;
+    sp24::GemmArgs g;
+    int st = check_gemm(values, meta, M, K, X, N, ldx, x_batch_stride, Y, ldy, y_batch_stride, batch, layout, 2, es, g);
+    if (st != SP24_OK) return st;
+    const bool tm = layout == SP24_TOKEN_MAJOR;
+    st = sp24::check_epilogue(bias, activation, R, ldr, Z, ldz, Y, ldy, tm ? M : N);
+    if (st != SP24_OK) return st;
+    if (batch > 1) {
+        const int64_t extent = tm ? (N - 1) * ldz + M : (M - 1) * ldz + N;
+        if ((R && r_batch_stride < 0) || (Z && z_batch_stride < extent)) return SP24_ERR_SHAPE;
+        if ((R && (r_batch_stride * es) % 16 != 0) || (Z && (z_batch_stride * es) % 16 != 0)) return SP24_ERR_ALIGN;
+        if (R == Y && r_batch_stride != y_batch_stride) return SP24_ERR_ARG;
+    }
+    g.out_fp32 = out_dtype == SP24_FP32;
+    g.epi.on = true;
+    g.epi.act = activation;
+    g.epi.bias = bias;
+    g.epi.R = R, g.epi.ldr = ldr, g.epi.sr = batch > 1 ? r_batch_stride : 0;
+    g.epi.Z = Z, g.epi.ldz = ldz, g.epi.sz = batch > 1 ? z_batch_stride : 0;
+    st = check_device();
+    if (st != SP24_OK) return st;
+    return hip_status(sp24::launch_gemm_bf16(g, static_cast<hipStream_t>(stream)));
 }
 
 int sp24_gemm_i8_ex(const int8_t* values, const uint8_t* meta, int64_t M, int64_t K, const int8_t* X, int64_t N,

@@ -9,6 +9,17 @@ namespace sp24 {
 // Output kinds of the int8 GEMM.
 enum OutKind { OUT_I32 = 0, OUT_F32 = 1, OUT_BF16 = 2, OUT_I8 = 3 };
 
+// Fused epilogue of a bf16 or 8-bit floating-point product (epilogue.h): bias (or NULL), activation (the sp24_activation
+// numbers), residual R and pre-activation Z (or NULL) of the output's type and layout, batch entries sr and sz apart.
+struct Epilogue {
+    bool on = false;
+    int act = 0;
+    const float* bias = nullptr;
+    const void* R = nullptr;
+    void* Z = nullptr;
+    int64_t ldr = 0, ldz = 0, sr = 0, sz = 0;
+};
+
 // Operands of one sparse GEMM call, validated by the C ABI. Element strides are in elements of the
 // operand's type.
 //   feature-major (tm == false): X is K x N (X[k, n] at k * ldx + n), Y is M x N (Y[m, n] at m * ldy + n)
@@ -33,6 +44,7 @@ struct GemmArgs {
     int gelu;
     int out_kind;
     float inv_scale;
+    Epilogue epi;        // bf16 only
 };
 
 hipError_t launch_col_norms(const uint16_t* X, int64_t K, int64_t N, int64_t ldx, float* norms, hipStream_t s);
@@ -64,6 +76,9 @@ bool gemm_bf16_fewtok_ok(const GemmArgs& g);
 hipError_t launch_gemm_bf16_fewtok(const GemmArgs& g, hipStream_t s);
 bool gemm_bf16_tiled_ok(const GemmArgs& g);
 hipError_t launch_gemm_bf16_tiled(const GemmArgs& g, hipStream_t s);
+// The tiled GEMM with a fused epilogue, `wide`: 256 x 256 tiles (else 256 x 128).
+hipError_t launch_gemm_bf16_fused_tm(const GemmArgs& g, bool wide, hipStream_t s);
+hipError_t launch_gemm_bf16_fused_fm(const GemmArgs& g, bool wide, hipStream_t s);
 
 // Dense reference with the token-major tiled kernel's tiling (measurement only): the weight converted to the
 // MFMA operand order, and the GEMM (token-major X, batch 1; values = the converted weight).
@@ -83,6 +98,9 @@ hipError_t launch_gemm_i8_tiled(const GemmArgs& g, hipStream_t s);
 
 // SP24_OK if the current device is gfx950, else SP24_ERR_DEVICE (sp24_api.cpp; cached per device).
 int check_device();
+// The operands of a fused epilogue: an sp24_status (layer_api.cpp). `length`: elements of a row of Y.
+int check_epilogue(const float* bias, int activation, const void* R, int64_t ldr, const void* Z, int64_t ldz, const void* Y, int64_t ldy,
+                   int64_t length);
 
 // 8-bit floating point (include/sp24_fp8.h). dtype: 0 BF16, 1 FP16, 2 FP32 (the sp24_dtype numbers).
 hipError_t launch_quant_fp8(const void* X, int dtype, int64_t N, int64_t K, int64_t ldx, uint8_t* codes, int64_t ldc,
@@ -107,9 +125,16 @@ struct Fp8GemmArgs {
     void* Y;
     int64_t M, K, N, ldx, lds, ldy;
     bool out_fp16;  // else bf16
+    Epilogue epi;
 };
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s);
 hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_fp8_tiled_fused(const Fp8GemmArgs& g, bool wide, hipStream_t s);
+
+// Gradient of the fused epilogue; parts: rows of M partial sums in the workspace (one: none are needed).
+int epilogue_back_parts(int64_t N, int64_t M);
+hipError_t launch_epilogue_back(const void* dY, int dtype, int64_t N, int64_t M, int64_t lddy, const void* Z, int64_t ldz, int act,
+                                void* dZ, int64_t lddz, float* dbias, void* workspace, hipStream_t s);
 
 // Weight gradient: dY N x M bf16, X N x K codes, dW M x K; meta NULL or the 2:4 pattern of dW.
 struct Fp8GradArgs {
