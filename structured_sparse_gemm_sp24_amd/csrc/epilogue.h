@@ -82,40 +82,48 @@ __device__ __forceinline__ raw4<OT> narrow4(const f32x4& y) {
     if constexpr (OT == T_FP32) return u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
     else return u32x2{pack16<OT == T_FP16>(y[0], y[1]), pack16<OT == T_FP16>(y[2], y[3])};
 }
-// Even: the address is a multiple of 8 (16-bit types) or 16 bytes and the line is not needed again here; else any element's.
-template <int OT, bool EVEN>
-__device__ __forceinline__ raw4<OT> read4(const char* p) {
-    if constexpr (EVEN) return __builtin_nontemporal_load(reinterpret_cast<const raw4<OT>*>(p));
-    else if constexpr (OT == T_FP32) return *reinterpret_cast<const u32x4_at4*>(p);
-    else return *reinterpret_cast<const u32x2_at2*>(p);
+// Memory of the operands as such: an address made from a number would else be of any kind, and its access a slower one.
+#define SP24_GLOBAL __attribute__((address_space(1)))
+typedef SP24_GLOBAL char global_char;
+template <typename T>
+__device__ __forceinline__ SP24_GLOBAL T* global_at(const char* p) { return (SP24_GLOBAL T*)p; }
+template <typename T>
+__device__ __forceinline__ SP24_GLOBAL T* global_at(const global_char* p) { return (SP24_GLOBAL T*)p; }
+
+// EVEN: the address is a multiple of 8 (16-bit types) or 16 bytes and the line is not needed again here; else any element's.
+template <int OT, bool EVEN, typename P>
+__device__ __forceinline__ raw4<OT> read4(P p) {
+    if constexpr (EVEN) return __builtin_nontemporal_load(global_at<const raw4<OT>>(p));
+    else if constexpr (OT == T_FP32) return *global_at<const u32x4_at4>(p);
+    else return *global_at<const u32x2_at2>(p);
 }
-template <int OT, bool EVEN>
-__device__ __forceinline__ void write4(char* p, const raw4<OT>& w) {
-    if constexpr (EVEN) __builtin_nontemporal_store(w, reinterpret_cast<raw4<OT>*>(p));
-    else if constexpr (OT == T_FP32) *reinterpret_cast<u32x4_at4*>(p) = w;
-    else *reinterpret_cast<u32x2_at2*>(p) = w;
+template <int OT, bool EVEN, typename P>
+__device__ __forceinline__ void write4(P p, const raw4<OT>& w) {
+    if constexpr (EVEN) __builtin_nontemporal_store(w, global_at<raw4<OT>>(p));
+    else if constexpr (OT == T_FP32) *global_at<u32x4_at4>(p) = w;
+    else *global_at<u32x2_at2>(p) = w;
 }
 // The first `in` of the four.
-template <int OT>
-__device__ __forceinline__ raw4<OT> read_in(const char* p, int in) {
+template <int OT, typename P>
+__device__ __forceinline__ raw4<OT> read_in(P p, int in) {
     if (in == 4) return read4<OT, false>(p);
     raw4<OT> w = {};
 #pragma unroll
     for (int t = 0; t < 3; t++)
         if (t < in) {
-            if constexpr (OT == T_FP32) w[t] = reinterpret_cast<const uint32_t*>(p)[t];
-            else w[t >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[t] << (16 * (t & 1));
+            if constexpr (OT == T_FP32) w[t] = global_at<const uint32_t>(p)[t];
+            else w[t >> 1] |= (uint32_t)global_at<const uint16_t>(p)[t] << (16 * (t & 1));
         }
     return w;
 }
-template <int OT>
-__device__ __forceinline__ void write_in(char* p, const raw4<OT>& w, int in) {
+template <int OT, typename P>
+__device__ __forceinline__ void write_in(P p, const raw4<OT>& w, int in) {
     if (in == 4) return write4<OT, false>(p, w);
 #pragma unroll
     for (int t = 0; t < 3; t++)
         if (t < in) {
-            if constexpr (OT == T_FP32) reinterpret_cast<uint32_t*>(p)[t] = w[t];
-            else reinterpret_cast<uint16_t*>(p)[t] = (uint16_t)(w[t >> 1] >> (16 * (t & 1)));
+            if constexpr (OT == T_FP32) global_at<uint32_t>(p)[t] = w[t];
+            else global_at<uint16_t>(p)[t] = (uint16_t)(w[t >> 1] >> (16 * (t & 1)));
         }
 }
 
@@ -125,6 +133,48 @@ struct Places {
     const char* R;
     int64_t ldy, ldz, ldr, rows, length;
 };
+
+// What a fused epilogue needs, in the arguments of a tiled kernel. Through the main loop a wave keeps it in one vector
+// register, a word a lane: in scalar registers it would push out others, and read again from the kernel's arguments, which
+// may lie in the host's memory, each tile would wait for it.
+struct Outputs {
+    char *Y, *Z;
+    const char* R;
+    const float* bias;
+    int64_t ldy, ldz, ldr, sy, sz, sr, M, N;  // strides of batch entries in elements
+    int64_t rows;  // WIDE: 16 rows of one take 2^31 bytes or more; EVEN: every row on 8 (16-bit types) or 16 bytes; else ODD
+};
+enum { WIDE, ODD, EVEN };
+constexpr int OUTPUT_WORDS = sizeof(Outputs) / 4;
+static_assert(OUTPUT_WORDS <= 64, "a word a lane");
+
+__device__ __forceinline__ uint32_t keep_outputs(const Outputs& o, int lane) {
+    uint32_t w = reinterpret_cast<const uint32_t*>(&o)[lane < OUTPUT_WORDS ? lane : 0];
+    asm volatile("" : "+v"(w));  // not read again
+    return w;
+}
+__device__ __forceinline__ Outputs kept_outputs(uint32_t kept) {
+    uint32_t w[OUTPUT_WORDS];
+#pragma unroll
+    for (int i = 0; i < OUTPUT_WORDS; i++) w[i] = (uint32_t)__builtin_amdgcn_readlane((int)kept, i);
+    return __builtin_bit_cast(Outputs, w);
+}
+inline Outputs outputs_of(const Epilogue& e, void* Y, int64_t ldy, int64_t sy, int64_t M, int64_t N, int es, int64_t batch) {
+    Outputs o{static_cast<char*>(Y), static_cast<char*>(e.Z), static_cast<const char*>(e.R), e.bias, ldy, e.ldz, e.ldr, sy, e.sz, e.sr, M, N, EVEN};
+    const auto look = [&](const void* p, int64_t ld, int64_t stride) {
+        if (p && ((ld * es) % (4 * es) != 0 || (batch > 1 && (stride * es) % (4 * es) != 0)) && o.rows == EVEN) o.rows = ODD;
+        if (p && ld * es * 16 >= ((int64_t)1 << 31)) o.rows = WIDE;
+    };
+    look(Y, ldy, sy);
+    look(e.R, e.ldr, e.sr);
+    look(e.Z, e.ldz, e.sz);
+    return o;
+}
+template <bool TM>
+__device__ __forceinline__ Places places_of(const Outputs& o, int64_t entry, int es) {
+    return {o.Y + entry * o.sy * es, o.Z ? o.Z + entry * o.sz * es : nullptr, o.R ? o.R + entry * o.sr * es : nullptr,
+            o.ldy, o.ldz, o.ldr, TM ? o.N : o.M, TM ? o.M : o.N};
+}
 
 // Places of batch entry `entry` (its Y given), for the kernels that need neither rows nor length.
 __device__ __forceinline__ Places places(const Epilogue& e, char* y, int64_t ldy, bool fp32, int64_t entry) {
@@ -140,32 +190,64 @@ inline Epilogue entries_from(Epilogue e, int64_t b0, bool fp32) {
     return e;
 }
 
-// The epilogue and the output of a kernel whose only argument has a member epi, Y, ldy, M and N, read here and not at the
-// kernel's start: kept in scalar registers through the main loop they would push out others.
-template <typename Args>
-__device__ __forceinline__ const __attribute__((address_space(4))) Args* late_args() {
-    auto k = (const __attribute__((address_space(4))) Args*)__builtin_amdgcn_kernarg_segment_ptr();
-    asm volatile("" : "+s"(k));
-    return k;
+// One output from z = acc + bias and its residual, the activation chosen at run time: the kernels for few tokens.
+__device__ __forceinline__ float residual1(const Places& p, int type, int64_t row, int64_t col) {
+    if (!p.R) return 0.f;
+    const int64_t o = row * p.ldr + col;
+    if (type == T_FP32) return reinterpret_cast<const float*>(p.R)[o];
+    const uint32_t r = reinterpret_cast<const uint16_t*>(p.R)[o];
+    return type == T_BF16 ? bf16_to_f32(r) : f16_to_f32(r);
 }
-
-// One output, the activation chosen at run time: the kernels for few tokens.
-__device__ __forceinline__ void finish1(const Epilogue& e, const Places& p, int type, float acc, float bias, int64_t row, int64_t col) {
-    const float z = e.bias ? acc + bias : acc;
-    float y = act_any(z, e.act);
-    const int64_t oy = row * p.ldy + col, oz = row * p.ldz + col, orr = row * p.ldr + col;
+__device__ __forceinline__ void finish1(int act, const Places& p, int type, float z, float r, int64_t row, int64_t col) {
+    float y = act_any(z, act);
+    if (p.R) y += r;
+    const int64_t oy = row * p.ldy + col, oz = row * p.ldz + col;
     if (type == T_FP32) {
-        if (p.R) y += reinterpret_cast<const float*>(p.R)[orr];
         if (p.Z) reinterpret_cast<float*>(p.Z)[oz] = z;
         reinterpret_cast<float*>(p.Y)[oy] = y;
     } else {
-        if (p.R) {
-            const uint32_t r = reinterpret_cast<const uint16_t*>(p.R)[orr];
-            y += type == T_BF16 ? bf16_to_f32(r) : f16_to_f32(r);
-        }
         if (p.Z) reinterpret_cast<uint16_t*>(p.Z)[oz] = (uint16_t)(type == T_BF16 ? pack16<false>(z, z) : pack16<true>(z, z));
         reinterpret_cast<uint16_t*>(p.Y)[oy] = (uint16_t)(type == T_BF16 ? pack16<false>(y, y) : pack16<true>(y, y));
     }
+}
+
+__device__ __forceinline__ f32x4 act_any4(f32x4 z, int act) {
+    f32x4 y = z;
+#pragma unroll
+    for (int t = 0; t < 4; t++) y[t] = act_any(z[t], act);
+    return y;
+}
+
+// Four consecutive outputs of a row from column col on, `in` of them inside, the activation chosen at run time; what they
+// need is requested apart, to be on its way during the last sums.
+template <int OT>
+struct Needed {
+    raw4<OT> r;
+    f32x4 b;
+};
+template <int OT>
+__device__ __forceinline__ Needed<OT> request4(const Epilogue& e, const Places& p, int64_t row, int64_t col, int in) {
+    Needed<OT> n = {};
+    if (p.R) n.r = read_in<OT>(p.R + (row * p.ldr + col) * (OT == T_FP32 ? 4 : 2), in);
+    if (e.bias) n.b = widen4<T_FP32>(read_in<T_FP32>(reinterpret_cast<const char*>(e.bias + col), in));
+    return n;
+}
+template <int OT>
+__device__ __forceinline__ void finish4(const Epilogue& e, const Places& p, const f32x4& acc, const Needed<OT>& n, int64_t row, int64_t col, int in) {
+    constexpr int ES = OT == T_FP32 ? 4 : 2;
+    const f32x4 z = acc + n.b;
+    f32x4 y = act_any4(z, e.act);
+    if (p.R) y += widen4<OT>(n.r);
+    if (p.Z) write_in<OT>(p.Z + (row * p.ldz + col) * ES, narrow4<OT>(z), in);
+    write_in<OT>(p.Y + (row * p.ldy + col) * ES, narrow4<OT>(y), in);
+}
+
+// The epilogue's arguments read at the kernel's start: where the compiler would read them, at its end, they are a trip to the
+// host's memory.
+__device__ __forceinline__ Epilogue read_early(const Epilogue& a) {
+    Epilogue e = a;
+    asm volatile("" : "+s"(e.bias), "+s"(e.R), "+s"(e.Z), "+s"(e.ldr), "+s"(e.ldz), "+s"(e.sr), "+s"(e.sz), "+s"(e.act));
+    return e;
 }
 
 // f(0) .. f(N - 1), each with its index as a constant (as a loop the compiler may refuse to unroll, and with it to keep
@@ -183,10 +265,13 @@ __device__ __forceinline__ void each(const F& f) {
     }
 }
 
-// A wave's place in one of Y, Z and R, four rows of it at a time. FULL: the wave's block lies inside, and every row on 8 or 16
-// bytes: a uniform address, 32-bit offsets of the lanes, and the lines are not needed again here. Otherwise an address a lane,
-// at any element.
-template <int OT, bool FULL>
+// How a wave's block lies in Y: wholly inside; with rows past the end; with columns past it too (or rows so long that 32-bit
+// offsets do not reach over 16 of them).
+enum { WHOLE, SOME_ROWS, ANYHOW };
+
+// A wave's place in one of Y, Z and R, four rows of it at a time: a uniform address and 32-bit offsets of the lanes, or ANYHOW an
+// address a lane.
+template <int OT, int BLOCK>
 struct Rows {
     static constexpr int ES = OT == T_FP32 ? 4 : 2;
     uint64_t at;
@@ -197,98 +282,205 @@ struct Rows {
         pitch = ld * ES;
         at = reinterpret_cast<uint64_t>(base) + (uint64_t)(row0 * pitch + col0 * ES);
         lane = (uint32_t)(row * pitch + col * ES);
-        if constexpr (!FULL) at += (uint64_t)(row * pitch + col * ES);
+        if constexpr (BLOCK != ANYHOW) asm volatile("" : "+v"(lane));  // 32 bits, not widened and added ahead
+        else at += (uint64_t)(row * pitch + col * ES);
     }
-    __device__ __forceinline__ char* place(int slot, int cols) const {
-        return reinterpret_cast<char*>(at + (uint64_t)(slot * pitch + cols * ES)) + (FULL ? lane : 0u);
+    __device__ __forceinline__ global_char* place(int slot, int cols) const {
+        return (global_char*)(at + (uint64_t)(slot * pitch + cols * ES)) + (BLOCK != ANYHOW ? lane : 0u);
     }
     // Sixteen rows on. The address is kept from the optimizer, which would else compute all of them ahead and run out of registers.
     __device__ __forceinline__ void advance() {
         at += (uint64_t)(16 * pitch);
-        if constexpr (FULL) asm volatile("" : "+s"(at));
+        if constexpr (BLOCK != ANYHOW) asm volatile("" : "+s"(at));
         else asm volatile("" : "+v"(at));
     }
-    __device__ __forceinline__ raw4<OT> read(int slot, int cols, int in) const {
-        if constexpr (FULL) return read4<OT, true>(place(slot, cols));
-        else return read_in<OT>(place(slot, cols), in);
+    // in: how many of the four elements exist (SOME_ROWS: none or all).
+    __device__ __forceinline__ void read(raw4<OT> (&v)[4], int cols, const int (&in)[4]) const {
+#pragma unroll
+        for (int s = 0; s < 4; s++) {
+            if constexpr (BLOCK == WHOLE) v[s] = read4<OT, false>(place(s, cols));
+            else if constexpr (BLOCK == SOME_ROWS) v[s] = in[s] ? read4<OT, false>(place(s, cols)) : raw4<OT>{};
+            else v[s] = read_in<OT>(place(s, cols), in[s]);
+        }
     }
-    __device__ __forceinline__ void write(int slot, int cols, const f32x4& v, int in) const {
-        if constexpr (FULL) write4<OT, true>(place(slot, cols), narrow4<OT>(v));
-        else write_in<OT>(place(slot, cols), narrow4<OT>(v), in);
+    // once: whole lines that are not needed again here go past the caches; where rows share lines the caches join the pieces.
+    __device__ __forceinline__ void write(const raw4<OT> (&v)[4], int cols, bool once, const int (&in)[4]) const {
+        if constexpr (BLOCK == ANYHOW) {
+#pragma unroll
+            for (int s = 0; s < 4; s++) write_in<OT>(place(s, cols), v[s], in[s]);
+        } else if constexpr (BLOCK == SOME_ROWS) {
+#pragma unroll
+            for (int s = 0; s < 4; s++)
+                if (in[s]) write4<OT, false>(place(s, cols), v[s]);
+        } else if (once) {
+            asm volatile("" ::: "memory");  // or the two branches become one, and the hint is lost
+#pragma unroll
+            for (int s = 0; s < 4; s++) write4<OT, true>(place(s, cols), v[s]);
+            asm volatile("" ::: "memory");
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; s++) write4<OT, false>(place(s, cols), v[s]);
+        }
     }
 };
 
+// Two 4 x 4 transposes inside the lane quads (quad_transpose of sp24_device.h) in half the instructions: the exchange between
+// two lanes and the choice of what to keep are one v_cndmask with a DPP source. Of two words on either side of the diagonal lane
+// b of a quad keeps its own and takes the other from lane b ^ 2, then b ^ 1. The s_nop, and further on the order, keep two
+// instructions between a register's write and its read through DPP. a and b must be results of vector instructions other
+// than matrix and transcendental ones, whose waits the compiler does not put before an asm block.
+__device__ __forceinline__ void quad_transpose2(uint32_t (&a)[4], uint32_t (&b)[4]) {
+    uint32_t o[8], x[8];
+    asm("s_nop 1\n\t"
+        "s_mov_b64 vcc, %24\n\t"
+        "v_cndmask_b32_dpp %8, %18, %16, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %9, %19, %17, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %12, %22, %20, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %13, %23, %21, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "s_not_b64 vcc, vcc\n\t"
+        "v_cndmask_b32_dpp %10, %16, %18, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %11, %17, %19, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %14, %20, %22, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %15, %21, %23, vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "s_mov_b64 vcc, %25\n\t"
+        "v_cndmask_b32_dpp %0, %9, %8, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %2, %11, %10, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %4, %13, %12, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %6, %15, %14, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "s_not_b64 vcc, vcc\n\t"
+        "v_cndmask_b32_dpp %1, %8, %9, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %3, %10, %11, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %5, %12, %13, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_cndmask_b32_dpp %7, %14, %15, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf"
+        : "=&v"(o[0]), "=&v"(o[1]), "=&v"(o[2]), "=&v"(o[3]), "=&v"(o[4]), "=&v"(o[5]), "=&v"(o[6]), "=&v"(o[7]), "=&v"(x[0]), "=&v"(x[1]),
+          "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]), "=&v"(x[6]), "=&v"(x[7])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "s"(0x3333333333333333ull),
+          "s"(0x5555555555555555ull)
+        : "vcc", "scc");
+#pragma unroll
+    for (int t = 0; t < 4; t++) a[t] = o[t], b[t] = o[4 + t];
+}
+
 // Epilogue of a wave's 128 channels x 16 FNT tokens from accumulators acc(i, j) whose lane (q, r) holds channels 16 i + 4 q
-// .. +3 of token 16 j + r. The transposes of the plain product's stores run on the fp32 sums, so that bias, activation and
-// residual all work on the four consecutive outputs of a row that a lane stores: token-major four channels of a token,
-// feature-major four tokens of a channel.
-template <bool TM, int OT, int ACT, bool FULL, int FNT, typename Acc>
-__device__ __forceinline__ void store_fused(const Acc& acc, const float* bias, const Places& p, int64_t mw, int64_t nw, int lane) {
-    constexpr int OUTER = TM ? FNT : 8, INNER = TM ? 2 : FNT / 4;  // groups of 16 rows, of 64 columns
+// .. +3 of token 16 j + r. The transposes of the plain product's stores run on the fp32 sums, so that activation and residual
+// work on the four consecutive outputs of a row that a lane stores: token-major four channels of a token, feature-major four
+// tokens of a channel. Groups of 16 rows x 64 columns, along a row first (token-major 256 consecutive bytes of a row go out
+// together: down the columns first 11008 x 4096 over 4096 tokens took 180 us without any epilogue, against 170). The residual of
+// a group is requested before the group in front of it is finished (HAS_R, 16-bit types, whole blocks; the other cases lack the
+// registers, and whether there is a residual is then seen group by group). The bias is added as the sums lie; where they
+// are results of vector instructions (VECTOR), after the transposes, which takes fewer registers.
+template <bool TM, bool VECTOR, int OT, int ACT, int BLOCK, bool HAS_R, int FNT, typename Acc>
+__device__ __forceinline__ void store_block(const Acc& acc, const float* bias, const Places& p, bool once, int64_t mw, int64_t nw, int lane) {
+    constexpr int ROWS = TM ? FNT : 8, COLS = TM ? 2 : FNT / 4, GROUPS = ROWS * COLS;
+    constexpr bool AHEAD = HAS_R && OT != T_FP32, LATE_BIAS = TM && VECTOR;
+    static_assert(BLOCK == WHOLE || !HAS_R, "residuals are looked for group by group");
     const int q = lane >> 4, r = lane & 15, x = r & 3, c = r >> 2;
     const int64_t row0 = TM ? nw : mw, col0 = TM ? mw : nw;
     const int row = TM ? 4 * c : 4 * q, col = TM ? 16 * x + 4 * q : 16 * x + 4 * c;
-    Rows<OT, FULL> y(p.Y, p.ldy, row0, col0, row, col), z(p.Z, p.ldz, row0, col0, row, col), res(p.R, p.ldr, row0, col0, row, col);
-    int64_t rows_left = p.rows - row0 - row, cols_left = p.length - col0 - col;  // from the lane's place on
-
-    f32x4 tb[TM ? 2 : 1] = {};  // token-major: the lane's channels
-    if constexpr (TM) {
-        if (bias) {
+    Rows<OT, BLOCK> y(p.Y, p.ldy, row0, col0, row, col), z(p.Z, p.ldz, row0, col0, row, col), res(p.R, p.ldr, row0, col0, row, col);
+    const int64_t cols_left = p.length - col0 - col, rows_left = p.rows - row0 - row;  // from the lane's place on
+    const auto inside = [&](int (&in)[4], int at_row, int at_col) __attribute__((always_inline)) {
+        const int64_t left = BLOCK == ANYHOW ? cols_left - 64 * at_col : 4;
+        const int cols = left >= 4 ? 4 : left <= 0 ? 0 : (int)left;
 #pragma unroll
-            for (int g = 0; g < 2; g++)
+        for (int s = 0; s < 4; s++) in[s] = BLOCK == WHOLE || rows_left > 16 * at_row + s ? cols : 0;
+    };
+    const auto bias_at = [&](int64_t m) __attribute__((always_inline)) {
+        const char* const at = reinterpret_cast<const char*>(bias + m);
+        const int64_t left = (TM ? p.length : p.rows) - m;
+        if constexpr (BLOCK == WHOLE || (BLOCK == SOME_ROWS && TM)) return widen4<T_FP32>(read4<T_FP32, false>(at));
+        return widen4<T_FP32>(read_in<T_FP32>(at, left <= 0 ? 0 : left < 4 ? (int)left : 4));
+    };
+    constexpr int BIAS = !TM ? 1 : LATE_BIAS ? 2 : 8;  // of the row of fragments, of the lane's columns, of its fragments
+    f32x4 b[BIAS] = {};
+    if (TM && bias) {
 #pragma unroll
-                for (int t = 0; t < 4; t++)
-                    if (FULL || cols_left > 64 * g + t) tb[g][t] = bias[col0 + col + 64 * g + t];
-        }
+        for (int f = 0; f < BIAS; f++) b[f] = bias_at(LATE_BIAS ? mw + 64 * f + col : mw + 16 * f + 4 * q);
     }
-    each<OUTER>([&](auto o) __attribute__((always_inline)) {
-        f32x4 fb = {0.f, 0.f, 0.f, 0.f};  // feature-major: the slots' channels
-        if constexpr (!TM) {
-            if (bias) {
-#pragma unroll
-                for (int s = 0; s < 4; s++)
-                    if (FULL || rows_left > s) fb[s] = bias[row0 + row + 16 * o + s];
-            }
+    raw4<OT> ahead[4];
+    const auto request = [&](auto g) __attribute__((always_inline)) {
+        int in[4];
+        inside(in, g.value / COLS, g.value % COLS);
+        if constexpr (g.value > 0 && g.value % COLS == 0) res.advance();
+        res.read(ahead, 64 * (g.value % COLS), in);
+    };
+    if constexpr (AHEAD) request(Index<0>());
+    each<GROUPS>([&](auto g) __attribute__((always_inline)) {
+        constexpr int at_row = g.value / COLS, at_col = g.value % COLS;
+        if constexpr (at_col == 0) {
+            if constexpr (g.value > 0) y.advance(), z.advance();
+            if (!TM && bias) b[0] = bias_at(mw + 16 * at_row + 4 * q);
         }
-        each<INNER>([&](auto g) __attribute__((always_inline)) {
-            int in[4];
-            raw4<OT> rv[4] = {};
-            if constexpr (!FULL) {
-                const int64_t left = cols_left - 64 * g;
-                const int cols = left >= 4 ? 4 : left <= 0 ? 0 : (int)left;
+        raw4<OT> now[4];
+        if constexpr (AHEAD) {
 #pragma unroll
-                for (int s = 0; s < 4; s++) in[s] = rows_left > s ? cols : 0;
-            }
-            if (p.R) {
+            for (int s = 0; s < 4; s++) now[s] = ahead[s];
+            if constexpr (g.value + 1 < GROUPS) request(Index<g.value + 1>());
+        }
+        uint32_t v[4][4];  // v[t][f]: the lane's value t of fragment f, then of slot f
 #pragma unroll
-                for (int s = 0; s < 4; s++) rv[s] = res.read(s, 64 * g, in[s]);
-            }
-            uint32_t v[4][4];
+        for (int f = 0; f < 4; f++) {
+            f32x4 a = TM ? acc(4 * at_col + f, at_row) : acc(at_row, 4 * at_col + f);
+            if constexpr (!LATE_BIAS) a += b[TM ? 4 * at_col + f : 0];
 #pragma unroll
-            for (int f = 0; f < 4; f++) {
-                const f32x4 a = TM ? acc(4 * g + f, o) : acc(o, 4 * g + f);
+            for (int t = 0; t < 4; t++) v[t][f] = __float_as_uint(a[t]);
+        }
+        if constexpr (!TM) {
+            uint32_t w[4][4];  // w[f][t]
 #pragma unroll
-                for (int t = 0; t < 4; t++) v[f][t] = __float_as_uint(a[t]);
-                if constexpr (!TM) quad_transpose(v[f], x);
-            }
-            slot_transpose4<4>(v, x);
+            for (int f = 0; f < 4; f++)
 #pragma unroll
-            for (int s = 0; s < 4; s++) {
-                f32x4 zv, yv;
+                for (int t = 0; t < 4; t++) w[f][t] = v[t][f];
+            quad_transpose2(w[0], w[1]);
+            quad_transpose2(w[2], w[3]);
 #pragma unroll
-                for (int t = 0; t < 4; t++) {
-                    zv[t] = __uint_as_float(v[s][t]) + (TM ? tb[TM ? g.value : 0][t] : fb[s]);
-                    yv[t] = act_f32<ACT>(zv[t]);
-                }
-                if (p.Z) z.write(s, 64 * g, zv, in[s]);
-                if (p.R) yv += widen4<OT>(rv[s]);
-                y.write(s, 64 * g, yv, in[s]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        });
-        y.advance(), z.advance(), res.advance();
-        if constexpr (!FULL) rows_left -= 16;
+            for (int f = 0; f < 4; f++)
+#pragma unroll
+                for (int t = 0; t < 4; t++) v[t][f] = w[f][t];
+        }
+        quad_transpose2(v[0], v[1]);
+        quad_transpose2(v[2], v[3]);
+        int in[4];
+        raw4<OT> out[4];
+        f32x4 zv[4], yv[4];
+        inside(in, at_row, at_col);
+#pragma unroll
+        for (int s = 0; s < 4; s++) {
+#pragma unroll
+            for (int t = 0; t < 4; t++) zv[s][t] = __uint_as_float(v[t][s]);
+            if constexpr (LATE_BIAS) zv[s] += b[at_col];
+        }
+        if (p.Z) {
+#pragma unroll
+            for (int s = 0; s < 4; s++) out[s] = narrow4<OT>(zv[s]);
+            z.write(out, 64 * at_col, once, in);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; s++)
+#pragma unroll
+            for (int t = 0; t < 4; t++) yv[s][t] = act_f32<ACT>(zv[s][t]);
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int s = 0; s < 4; s++) yv[s] += widen4<OT>(now[s]);
+        } else if (HAS_R || (BLOCK != WHOLE && p.R)) {
+            request(g);
+#pragma unroll
+            for (int s = 0; s < 4; s++) yv[s] += widen4<OT>(ahead[s]);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; s++) out[s] = narrow4<OT>(yv[s]);
+        y.write(out, 64 * at_col, once, in);
+        __builtin_amdgcn_sched_barrier(0);
     });
+}
+
+template <bool TM, bool VECTOR, int OT, int ACT, int FNT, typename Acc>
+__device__ __forceinline__ void store_fused(const Acc& acc, const Outputs& o, const Places& p, int64_t mw, int64_t nw, int lane) {
+    const bool rows = TM ? nw + 16 * FNT <= o.N : mw + 128 <= o.M, cols = (TM ? mw + 128 <= o.M : nw + 16 * FNT <= o.N) && o.rows != WIDE;
+    if (!cols) store_block<TM, VECTOR, OT, ACT, ANYHOW, false, FNT>(acc, o.bias, p, false, mw, nw, lane);
+    else if (!rows) store_block<TM, VECTOR, OT, ACT, SOME_ROWS, false, FNT>(acc, o.bias, p, false, mw, nw, lane);
+    else if (p.R) store_block<TM, VECTOR, OT, ACT, WHOLE, true, FNT>(acc, o.bias, p, o.rows == EVEN, mw, nw, lane);
+    else store_block<TM, VECTOR, OT, ACT, WHOLE, false, FNT>(acc, o.bias, p, o.rows == EVEN, mw, nw, lane);
 }
 
 }  // namespace sp24

@@ -38,7 +38,7 @@ struct DirectArgs {
     Epilogue epi;
 };
 
-template <int NF>
+template <int NF, bool EPI>
 __global__ __launch_bounds__(256) void gemm_bf16_direct(DirectArgs d) {
     const int lane = threadIdx.x & 63;
     const int r = lane & 15, q = lane >> 4;
@@ -90,9 +90,11 @@ __global__ __launch_bounds__(256) void gemm_bf16_direct(DirectArgs d) {
         for (int i = 0; i < 4; i++) {
             const int64_t m = m0 + 4 * q + i;
             if (m >= d.M) continue;
-            if (d.epi.on) {
-                finish1(d.epi, places(d.epi, Y, d.tm ? d.syn : d.sym, d.out_fp32, blockIdx.z), d.out_fp32 ? T_FP32 : T_BF16, acc[f][i],
-                        d.epi.bias ? d.epi.bias[m] : 0.f, d.tm ? n : m, d.tm ? m : n);
+            if constexpr (EPI) {
+                const Places p = places(d.epi, Y, d.tm ? d.syn : d.sym, d.out_fp32, blockIdx.z);
+                const int type = d.out_fp32 ? T_FP32 : T_BF16;
+                const int64_t row = d.tm ? n : m, col = d.tm ? m : n;
+                finish1(d.epi.act, p, type, acc[f][i] + (d.epi.bias ? d.epi.bias[m] : 0.f), residual1(p, type, row, col), row, col);
                 continue;
             }
             const int64_t o = m * d.sym + n * d.syn;
@@ -104,6 +106,7 @@ __global__ __launch_bounds__(256) void gemm_bf16_direct(DirectArgs d) {
     }
 }
 
+template <bool EPI>
 static hipError_t launch_gemm_bf16_direct(const GemmArgs& g, hipStream_t s) {
     DirectArgs d;
     d.vals = static_cast<const uint16_t*>(g.values);
@@ -129,9 +132,9 @@ static hipError_t launch_gemm_bf16_direct(const GemmArgs& g, hipStream_t s) {
         e.Y = static_cast<char*>(d.Y) + b0 * d.syb * (g.out_fp32 ? 4 : 2);
         e.epi = entries_from(d.epi, b0, g.out_fp32);
         if (g.N <= 16)
-            hipLaunchKernelGGL(gemm_bf16_direct<1>, dim3((unsigned)((g.N + 15) / 16), gy, gz), dim3(256), 0, s, e);
+            hipLaunchKernelGGL((gemm_bf16_direct<1, EPI>), dim3((unsigned)((g.N + 15) / 16), gy, gz), dim3(256), 0, s, e);
         else
-            hipLaunchKernelGGL(gemm_bf16_direct<4>, dim3((unsigned)((g.N + 63) / 64), gy, gz), dim3(256), 0, s, e);
+            hipLaunchKernelGGL((gemm_bf16_direct<4, EPI>), dim3((unsigned)((g.N + 63) / 64), gy, gz), dim3(256), 0, s, e);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
@@ -142,7 +145,7 @@ hipError_t launch_gemm_bf16(const GemmArgs& g, hipStream_t s) {
     if (gemm_bf16_fewtok_ok(g)) return launch_gemm_bf16_fewtok(g, s);
     if (gemm_bf16_skinny_ok(g)) return launch_gemm_bf16_skinny(g, s);
     if (gemm_bf16_tiled_ok(g)) return launch_gemm_bf16_tiled(g, s);
-    return launch_gemm_bf16_direct(g, s);
+    return g.epi.on ? launch_gemm_bf16_direct<true>(g, s) : launch_gemm_bf16_direct<false>(g, s);
 }
 
 }  // namespace sp24

@@ -76,7 +76,7 @@ __device__ __forceinline__ int tm_swz(int n) { return ((n >> 1) & 7) ^ ((n & 1) 
 typedef __attribute__((address_space(3))) char lds_char;
 typedef const __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-template <int S, int D, int XR>
+template <int S, int D, int XR, bool EPI>
 __global__ __launch_bounds__(64 * S) void gemm_bf16_fewtok(Args g) {
     static_assert(XR == 2 || XR == 8 || XR == 16, "X tile rows");
     constexpr int NXI = XR == 16 ? 2 : 1;           // X loads per unit (one dword load for 2 rows)
@@ -97,6 +97,9 @@ __global__ __launch_bounds__(64 * S) void gemm_bf16_fewtok(Args g) {
     const int64_t t0 = T * wave / S, t1 = T * (wave + 1) / S;
     const int64_t tf = t1 < Tf ? t1 : Tf;         // the ring takes the full tiles [t0, tf)
     const int n = (int)(tf > t0 ? tf - t0 : 0);
+
+    Epilogue epi;
+    if constexpr (EPI) epi = read_early(g.epi);
 
     const i32x4 rA = make_rsrc(g.vals + b * T * 1024, T * 1024);
     const i32x4 rM = make_rsrc(g.meta + b * T * 128, T * 128);
@@ -178,13 +181,27 @@ __global__ __launch_bounds__(64 * S) void gemm_bf16_fewtok(Args g) {
                                                         acc, (int)idx, 0, 0);
     }
 
+    // what the epilogue adds, on its way during the last sums (a thread has one output at most)
+    char* const Y = static_cast<char*>(g.Y) + (int64_t)blockIdx.y * g.syb * (g.out_fp32 ? 4 : 2);
+    const Places at = places(epi, Y, g.ldy, g.out_fp32, blockIdx.y);
+    const int type = g.out_fp32 ? T_FP32 : T_BF16;
+    static_assert(64 * S >= 256, "one output a thread");
+    float bias = 0.f, res = 0.f;
+    if (EPI && threadIdx.x < 256) {
+        const int64_t m = b * 16 + threadIdx.x % 16;
+        const int col = threadIdx.x / 16;
+        if (m < M && col < N) {
+            if (epi.bias) bias = epi.bias[m];
+            res = residual1(at, type, col, m);
+        }
+    }
+
     // sum the S partial tiles in wave order: lane (r, q) holds column r, rows 4q .. 4q+3 of the block
     __syncthreads();  // every wave is done with its ring
     float* const red = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < 4; i++) red[wave * 256 + (4 * q + i) * 16 + r] = acc[i];
     __syncthreads();
-    char* const Y = static_cast<char*>(g.Y) + (int64_t)blockIdx.y * g.syb * (g.out_fp32 ? 4 : 2);
     for (int e = threadIdx.x; e < 256; e += 64 * S) {
         // consecutive threads take consecutive rows m of one token row of Y (N x M)
         const int row = e % 16, col = e / 16;
@@ -194,8 +211,8 @@ __global__ __launch_bounds__(64 * S) void gemm_bf16_fewtok(Args g) {
         const int64_t m = b * 16 + row;
         if (m < M && col < N) {
             const int64_t o = (int64_t)col * g.ldy + m;
-            if (g.epi.on)
-                finish1(g.epi, places(g.epi, Y, g.ldy, g.out_fp32, blockIdx.y), g.out_fp32 ? T_FP32 : T_BF16, s, g.epi.bias ? g.epi.bias[m] : 0.f, col, m);
+            if (EPI)
+                finish1(epi.act, at, type, s + bias, res, col, m);
             else if (g.out_fp32)
                 reinterpret_cast<float*>(Y)[o] = s;
             else
@@ -204,8 +221,8 @@ __global__ __launch_bounds__(64 * S) void gemm_bf16_fewtok(Args g) {
     }
 }
 
-template <int S, int D, int XR>
-hipError_t launch(const GemmArgs& g, hipStream_t s) {
+template <int S, int D, int XR, bool EPI>
+hipError_t launch_as(const GemmArgs& g, hipStream_t s) {
     Args a;
     a.vals = static_cast<const uint8_t*>(g.values);
     a.meta = g.meta;
@@ -223,11 +240,16 @@ hipError_t launch(const GemmArgs& g, hipStream_t s) {
         e.X = a.X + b0 * a.sxb;
         e.Y = static_cast<char*>(a.Y) + b0 * a.syb * (g.out_fp32 ? 4 : 2);
         e.epi = entries_from(a.epi, b0, g.out_fp32);
-        hipLaunchKernelGGL((gemm_bf16_fewtok<S, D, XR>), dim3(grid, gb), dim3(64 * S), 0, s, e);
+        hipLaunchKernelGGL((gemm_bf16_fewtok<S, D, XR, EPI>), dim3(grid, gb), dim3(64 * S), 0, s, e);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
     return hipSuccess;
+}
+
+template <int S, int D, int XR>
+hipError_t launch(const GemmArgs& g, hipStream_t s) {
+    return g.epi.on ? launch_as<S, D, XR, true>(g, s) : launch_as<S, D, XR, false>(g, s);
 }
 
 }  // namespace fewtok

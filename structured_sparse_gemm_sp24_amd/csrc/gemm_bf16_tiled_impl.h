@@ -133,8 +133,8 @@ struct Args {
     int64_t M, K, N, ldx, ldy;
     int64_t sxb, syb;  // batch strides (elements)
     int tilesM, tilesN, batch;
-    int y_vec;  // Y (and R and Z) base and row pitch allow 8-byte (bf16) / 16-byte (fp32) stores, 4 rows < 2^31 bytes
-    Epilogue epi;
+    int y_vec;  // Y base and row pitch allow 8-byte (bf16) / 16-byte (fp32) stores, 4 rows < 2^31 bytes
+    Outputs out;  // with a fused epilogue
 };
 
 // Where the loads of one tile come from: its corner and the buffer descriptors of its compressed
@@ -630,22 +630,13 @@ __device__ __forceinline__ void store_tile_tm(const f32x4 (&acc)[FM][FNT], const
 
 // A wave's outputs through the fused epilogue (epilogue.h).
 template <bool TM, bool OUT_FP32, int ACT, int FNT>
-__device__ __forceinline__ void store_fused_tile(const f32x4 (&acc)[FM][FNT], int entry, int64_t mw, int64_t nw, int lane) {
-    constexpr int OT = OUT_FP32 ? T_FP32 : T_BF16, ES = OUT_FP32 ? 4 : 2;
-    const auto* const k = late_args<Args>();
-    char* const Z = static_cast<char*>(k->epi.Z);
-    const char* const R = static_cast<const char*>(k->epi.R);
-    const int64_t M = k->M, N = k->N;
-    Places p;
-    p.Y = static_cast<char*>(k->Y) + entry * k->syb * ES;
-    p.Z = Z ? Z + entry * k->epi.sz * ES : nullptr;
-    p.R = R ? R + entry * k->epi.sr * ES : nullptr;
-    p.ldy = k->ldy, p.ldz = k->epi.ldz, p.ldr = k->epi.ldr;
-    p.rows = TM ? N : M;
-    p.length = TM ? M : N;
+__device__ __forceinline__ void store_fused_tile(const f32x4 (&acc)[FM][FNT], uint32_t kept, int entry, int64_t mw, int64_t nw, int lane) {
+    constexpr int OT = OUT_FP32 ? T_FP32 : T_BF16;
+    const Outputs o = kept_outputs(kept);
+    const Places p = places_of<TM>(o, entry, OUT_FP32 ? 4 : 2);
     const auto at = [&](int i, int j) __attribute__((always_inline)) { return acc[i][j]; };
-    if (mw + WM <= M && nw + 16 * FNT <= N && k->y_vec) store_fused<TM, OT, ACT, true, FNT>(at, k->epi.bias, p, mw, nw, lane);
-    else store_fused<TM, OT, ACT, false, FNT>(at, k->epi.bias, p, mw, nw, lane);
+    static_assert(WM == 128 && FM == 8, "a wave's block");
+    store_fused<TM, false, OT, ACT, FNT>(at, o, p, mw, nw, lane);
 }
 
 // The feature-major loop (X K x N): 256 x 256 tiles with four waves of 128 x 128, or 256 x 128 tiles with two
@@ -661,6 +652,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
     const int p = blockIdx.x;
     int L = tile_of(a, p, 0);
     if (L < 0) return;  // whole workgroup
+    uint32_t kept = 0;
+    if constexpr (ACT != NO_EPILOGUE) kept = keep_outputs(a.out, threadIdx.x & 63);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm0 = (wave / 2) * WM, wn0 = (wave % 2) * C::WN;
     const LaneOffsets<F, C::B_ROW> o = lane_offsets<false, F, C::B_ROW>(wm0, wn0, lane);
@@ -711,7 +704,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
         {
             const int64_t mw = cur_t.m0 + wm0, nw = cur_t.n0 + wn0;
             if constexpr (ACT != NO_EPILOGUE)
-                store_fused_tile<false, OUT_FP32, ACT>(acc, cur_t.entry, mw, nw, lane);
+                store_fused_tile<false, OUT_FP32, ACT>(acc, kept, cur_t.entry, mw, nw, lane);
             else if ((mw + WM <= a.M) && (nw + C::WN <= a.N) && a.y_vec)
                 store_tile<OUT_FP32, true>(acc, a, cur_t.y, mw, nw, lane);
             else
@@ -888,6 +881,8 @@ __global__ __launch_bounds__(64 * TmCfg<BN>::WAVES) __attribute__((amdgpu_waves_
     const int p = blockIdx.x;
     int Lt = tile_of(a, p, 0);
     if (Lt < 0) return;
+    uint32_t kept = 0;
+    if constexpr (ACT != NO_EPILOGUE) kept = keep_outputs(a.out, threadIdx.x & 63);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm0 = (wave / (W / 2)) * WM, wn0 = (wave % (W / 2)) * C::WN;
     const LaneOffsets<4, 256> o = lane_offsets<true, 4, 256>(wm0, wn0, lane);
@@ -937,7 +932,7 @@ __global__ __launch_bounds__(64 * TmCfg<BN>::WAVES) __attribute__((amdgpu_waves_
         {
             const int64_t mw = cur_t.m0 + wm0, nw = cur_t.n0 + wn0;
             if constexpr (ACT != NO_EPILOGUE)
-                store_fused_tile<true, OUT_FP32, ACT>(acc, cur_t.entry, mw, nw, lane);
+                store_fused_tile<true, OUT_FP32, ACT>(acc, kept, cur_t.entry, mw, nw, lane);
             else if ((mw + WM <= a.M) && (nw + C::WN <= a.N) && a.y_vec)
                 store_tile_tm<OUT_FP32, true>(acc, a, cur_t.y, mw, nw, lane);
             else
@@ -975,13 +970,7 @@ static hipError_t launch_bn(const GemmArgs& g, hipStream_t s) {
     const int64_t es = g.out_fp32 ? 4 : 2;
     a.y_vec = ((reinterpret_cast<uintptr_t>(g.Y) & 15) == 0) && ((g.ldy * es) % 16 == 0) &&
               (g.batch == 1 || (g.sy * es) % 16 == 0) && g.ldy * es * 16 < ((int64_t)1 << 31);
-    a.epi = g.epi;
-    if constexpr (ACT != NO_EPILOGUE) {
-        const auto rows_ok = [&](const void* p, int64_t ld, int64_t stride) {
-            return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * es) % 16 == 0 && (g.batch == 1 || (stride * es) % 16 == 0) && ld * es * 16 < ((int64_t)1 << 31));
-        };
-        a.y_vec = a.y_vec && rows_ok(g.epi.R, g.epi.ldr, g.epi.sr) && rows_ok(g.epi.Z, g.epi.ldz, g.epi.sz);
-    }
+    if constexpr (ACT != NO_EPILOGUE) a.out = outputs_of(g.epi, g.Y, g.ldy, g.sy, g.M, g.N, (int)es, g.batch);
     const int T = a.tilesM * a.tilesN * a.batch;
     const int S = (int)((g.K + tiled_bf16::BK - 1) / tiled_bf16::BK);
     // workgroups walking several tiles, OCC per compute unit (the eight-wave token-major workgroup fills a CU

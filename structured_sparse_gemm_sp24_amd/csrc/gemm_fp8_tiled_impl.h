@@ -69,8 +69,8 @@ struct Args {
     int64_t M, K, N, ldx, lds, ldy;
     int S;  // stages
     int tilesM, tilesN;
-    int y_vec;  // every row of Y (and of R and Z) starts on 8 bytes
-    Epilogue epi;
+    int y_vec;  // every row of Y starts on 8 bytes
+    Outputs out;  // with a fused epilogue
 };
 
 __device__ __forceinline__ i32x4 make_rsrc(const void* base, int64_t bytes) {
@@ -488,15 +488,10 @@ __device__ __forceinline__ void store_tile(const f32x4 (&acc)[FM][FN], const Uni
         }
 }
 
-__device__ __forceinline__ Places places_of(const Args& a) {
-    const Epilogue& e = a.epi;
-    return {static_cast<char*>(a.Y), static_cast<char*>(e.Z), static_cast<const char*>(e.R), a.ldy, e.ldz, e.ldr, a.N, a.M};
-}
-
 // The wave's tile at (mw, nw) from memory: each block's products from zero and added with their own scale, 16 rows at a
 // time.
 template <bool F16, int ACT>
-__device__ __forceinline__ void sum_apart(const Args& a, int64_t mw, int64_t nw) {
+__device__ __forceinline__ void sum_apart(const Args& a, uint32_t kept, int64_t mw, int64_t nw) {
     const int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));  // nothing kept for this
     const int q = lane >> 4, r = lane & 15, S = a.S;
     const int64_t xb = (a.N - 1 - nw) * a.ldx + a.K;
@@ -539,10 +534,13 @@ __device__ __forceinline__ void sum_apart(const Args& a, int64_t mw, int64_t nw)
         for (int j = 0; j < FN; j++) {
             const int64_t n = nw + 16 * j + r;
             if constexpr (ACT != NO_EPILOGUE) {
+                constexpr int OT = F16 ? T_FP16 : T_BF16;
+                const Outputs o = kept_outputs(kept);
+                const Places p = places_of<true>(o, 0, 2);
 #pragma unroll
                 for (int c = 0; c < 4; c++)
                     if (n < a.N && m + c < a.M)
-                        finish1(a.epi, places_of(a), F16 ? T_FP16 : T_BF16, acc[j][c], a.epi.bias ? a.epi.bias[m + c] : 0.f, n, m + c);
+                        finish1(ACT, p, OT, acc[j][c] + (o.bias ? o.bias[m + c] : 0.f), residual1(p, OT, n, m + c), n, m + c);
                 continue;
             }
             const uint32_t y[2] = {pack16<F16>(acc[j][0], acc[j][1]), pack16<F16>(acc[j][2], acc[j][3])};
@@ -562,6 +560,8 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
     const int p = blockIdx.x, S = a.S;
     Tile cur = tile_of<BN>(a, p, 0);
     if (!cur.valid) return;  // whole workgroup
+    uint32_t kept = 0;
+    if constexpr (ACT != NO_EPILOGUE) kept = keep_outputs(a.out, threadIdx.x & 63);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
     const int wm0 = (wave & 1) * WM, wn0 = (wave >> 1) * WN;
     const LoadOffsets lo = load_offsets(a, lane);
@@ -610,10 +610,10 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
                 return y;
             };
             constexpr int OT = F16 ? T_FP16 : T_BF16;
-            const auto* const e = late_args<Args>();
-            const Places to{static_cast<char*>(e->Y), static_cast<char*>(e->epi.Z), static_cast<const char*>(e->epi.R), e->ldy, e->epi.ldz, e->epi.ldr, e->N, e->M};
-            if (mw + WM <= to.length && nw + WN <= to.rows && e->y_vec) store_fused<true, OT, ACT, true, FN>(at, e->epi.bias, to, mw, nw, lane);
-            else store_fused<true, OT, ACT, false, FN>(at, e->epi.bias, to, mw, nw, lane);
+            const Outputs out = kept_outputs(kept);
+            const Places to = places_of<true>(out, 0, 2);
+            static_assert(WM == 128 && FM == 8, "a wave's block");
+            store_fused<true, true, OT, ACT, FN>(at, out, to, mw, nw, lane);
         } else if (mw + WM > a.M || nw + WN > a.N) store_tile<F16, EDGE>(acc, g.u, a, mw, nw, lane);
         else if (a.y_vec) store_tile<F16, EVEN_PITCH>(acc, g.u, a, mw, nw, lane);
         else store_tile<F16, ODD_PITCH>(acc, g.u, a, mw, nw, lane);
@@ -632,7 +632,7 @@ __global__ __launch_bounds__(64 * Cfg<BN>::WAVES) __attribute__((amdgpu_waves_pe
     for (int k = 0; apart != 0; k++) {
         const Tile t = tile_of<BN>(a, p, k);
         if (!t.valid) break;
-        if ((apart >> (k & 63)) & 1 && t.n0 + wn0 < a.N) sum_apart<F16, ACT>(a, t.m0 + wm0, t.n0 + wn0);
+        if ((apart >> (k & 63)) & 1 && t.n0 + wn0 < a.N) sum_apart<F16, ACT>(a, kept, t.m0 + wm0, t.n0 + wn0);
     }
 }
 
@@ -644,9 +644,8 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
     a.S = (int)((g.K + BK - 1) / BK);
     a.tilesM = (int)((g.M + BM - 1) / BM);
     a.tilesN = (int)((g.N + BN - 1) / BN);
-    a.epi = g.epi;
-    // Y, R and Z are 16-byte aligned
-    a.y_vec = g.ldy % 4 == 0 && (ACT == NO_EPILOGUE || ((!g.epi.R || g.epi.ldr % 4 == 0) && (!g.epi.Z || g.epi.ldz % 4 == 0)));
+    a.y_vec = g.ldy % 4 == 0;  // Y is 16-byte aligned
+    if constexpr (ACT != NO_EPILOGUE) a.out = outputs_of(g.epi, g.Y, g.ldy, 0, g.M, g.N, 2, 1);
     const int64_t T = (int64_t)a.tilesM * a.tilesN;
     // as many workgroups as fit walk the tiles; one tile each where a tile has a single stage (the pipeline across
     // tiles needs both buffers within one tile)

@@ -67,6 +67,7 @@ hipError_t launch_decompress(const void* values, const uint8_t* meta, int dtype,
 hipError_t launch_gemm_bf16(const GemmArgs& g, hipStream_t s);
 bool gemm_bf16_skinny_ok(const GemmArgs& g);
 hipError_t launch_gemm_bf16_skinny(const GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_bf16_skinny_fused(const GemmArgs& g, hipStream_t s);
 // Compute units of the current device (cached per device; 256 if the query fails).
 int device_cus();
 // Workgroup tile width (256, or 128 for token-major X) of a tiled int8 GEMM launch.
@@ -128,6 +129,7 @@ struct Fp8GemmArgs {
     Epilogue epi;
 };
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_fp8_fewtok_fused(const Fp8GemmArgs& g, hipStream_t s);
 hipError_t launch_gemm_fp8_tiled(const Fp8GemmArgs& g, hipStream_t s);
 hipError_t launch_gemm_fp8_tiled_fused(const Fp8GemmArgs& g, bool wide, hipStream_t s);
 
