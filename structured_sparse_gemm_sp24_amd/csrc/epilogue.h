@@ -142,9 +142,13 @@ struct Outputs {
     const char* R;
     const float* bias;
     int64_t ldy, ldz, ldr, sy, sz, sr, M, N;  // strides of batch entries in elements
-    int64_t rows;  // WIDE: 16 rows of one take 2^31 bytes or more; EVEN: every row on 8 (16-bit types) or 16 bytes; else ODD
+    int64_t rows;  // one of these
 };
-enum { WIDE, ODD, EVEN };
+// Rows of Y, Z and R: 16 of one take 2^31 bytes or more; every one on 8 (16-bit types) or 16 bytes, and then the whole of Y takes
+// 64 MB or more; else ODD. A residual is usually what was written last: a small one is read through the caches, which may
+// still hold it (768 x 768 over 6304 tokens 16.4 us against 18.0, 512 x 128 over 32 x 784 23.8 against 31.3, buffers in turn), a large
+// one past them (11008 x 4096 over 4096 tokens 187 against 195).
+enum { WIDE, ODD, EVEN, EVEN_LARGE };
 constexpr int OUTPUT_WORDS = sizeof(Outputs) / 4;
 static_assert(OUTPUT_WORDS <= 64, "a word a lane");
 
@@ -168,6 +172,7 @@ inline Outputs outputs_of(const Epilogue& e, void* Y, int64_t ldy, int64_t sy, i
     look(Y, ldy, sy);
     look(e.R, e.ldr, e.sr);
     look(e.Z, e.ldz, e.sz);
+    if (o.rows == EVEN && M * N * batch * es >= ((int64_t)64 << 20)) o.rows = EVEN_LARGE;
     return o;
 }
 template <bool TM>
@@ -294,8 +299,16 @@ struct Rows {
         if constexpr (BLOCK != ANYHOW) asm volatile("" : "+s"(at));
         else asm volatile("" : "+v"(at));
     }
-    // in: how many of the four elements exist (SOME_ROWS: none or all).
-    __device__ __forceinline__ void read(raw4<OT> (&v)[4], int cols, const int (&in)[4]) const {
+    // in: how many of the four elements exist (SOME_ROWS: none or all). once: whole lines that are not needed again here go past
+    // the caches; where rows share lines the caches join the pieces.
+    __device__ __forceinline__ void read(raw4<OT> (&v)[4], int cols, bool once, const int (&in)[4]) const {
+        if (BLOCK == WHOLE && once) {
+            asm volatile("" ::: "memory");  // or the two branches become one, and the hint is lost
+#pragma unroll
+            for (int s = 0; s < 4; s++) v[s] = read4<OT, true>(place(s, cols));
+            asm volatile("" ::: "memory");
+            return;
+        }
 #pragma unroll
         for (int s = 0; s < 4; s++) {
             if constexpr (BLOCK == WHOLE) v[s] = read4<OT, false>(place(s, cols));
@@ -303,7 +316,6 @@ struct Rows {
             else v[s] = read_in<OT>(place(s, cols), in[s]);
         }
     }
-    // once: whole lines that are not needed again here go past the caches; where rows share lines the caches join the pieces.
     __device__ __forceinline__ void write(const raw4<OT> (&v)[4], int cols, bool once, const int (&in)[4]) const {
         if constexpr (BLOCK == ANYHOW) {
 #pragma unroll
@@ -313,7 +325,7 @@ struct Rows {
             for (int s = 0; s < 4; s++)
                 if (in[s]) write4<OT, false>(place(s, cols), v[s]);
         } else if (once) {
-            asm volatile("" ::: "memory");  // or the two branches become one, and the hint is lost
+            asm volatile("" ::: "memory");  // as above
 #pragma unroll
             for (int s = 0; s < 4; s++) write4<OT, true>(place(s, cols), v[s]);
             asm volatile("" ::: "memory");
@@ -370,7 +382,7 @@ __device__ __forceinline__ void quad_transpose2(uint32_t (&a)[4], uint32_t (&b)[
 // registers, and whether there is a residual is then seen group by group). The bias is added as the sums lie; where they
 // are results of vector instructions (VECTOR), after the transposes, which takes fewer registers.
 template <bool TM, bool VECTOR, int OT, int ACT, int BLOCK, bool HAS_R, int FNT, typename Acc>
-__device__ __forceinline__ void store_block(const Acc& acc, const float* bias, const Places& p, bool once, int64_t mw, int64_t nw, int lane) {
+__device__ __forceinline__ void store_block(const Acc& acc, const float* bias, const Places& p, int64_t how, int64_t mw, int64_t nw, int lane) {
     constexpr int ROWS = TM ? FNT : 8, COLS = TM ? 2 : FNT / 4, GROUPS = ROWS * COLS;
     constexpr bool AHEAD = HAS_R && OT != T_FP32, LATE_BIAS = TM && VECTOR;
     static_assert(BLOCK == WHOLE || !HAS_R, "residuals are looked for group by group");
@@ -402,7 +414,7 @@ __device__ __forceinline__ void store_block(const Acc& acc, const float* bias, c
         int in[4];
         inside(in, g.value / COLS, g.value % COLS);
         if constexpr (g.value > 0 && g.value % COLS == 0) res.advance();
-        res.read(ahead, 64 * (g.value % COLS), in);
+        res.read(ahead, 64 * (g.value % COLS), how == EVEN_LARGE, in);
     };
     if constexpr (AHEAD) request(Index<0>());
     each<GROUPS>([&](auto g) __attribute__((always_inline)) {
@@ -453,7 +465,7 @@ __device__ __forceinline__ void store_block(const Acc& acc, const float* bias, c
         if (p.Z) {
 #pragma unroll
             for (int s = 0; s < 4; s++) out[s] = narrow4<OT>(zv[s]);
-            z.write(out, 64 * at_col, once, in);
+            z.write(out, 64 * at_col, how >= EVEN, in);
         }
 #pragma unroll
         for (int s = 0; s < 4; s++)
@@ -469,7 +481,7 @@ __device__ __forceinline__ void store_block(const Acc& acc, const float* bias, c
         }
 #pragma unroll
         for (int s = 0; s < 4; s++) out[s] = narrow4<OT>(yv[s]);
-        y.write(out, 64 * at_col, once, in);
+        y.write(out, 64 * at_col, how >= EVEN, in);
         __builtin_amdgcn_sched_barrier(0);
     });
 }
@@ -477,10 +489,10 @@ __device__ __forceinline__ void store_block(const Acc& acc, const float* bias, c
 template <bool TM, bool VECTOR, int OT, int ACT, int FNT, typename Acc>
 __device__ __forceinline__ void store_fused(const Acc& acc, const Outputs& o, const Places& p, int64_t mw, int64_t nw, int lane) {
     const bool rows = TM ? nw + 16 * FNT <= o.N : mw + 128 <= o.M, cols = (TM ? mw + 128 <= o.M : nw + 16 * FNT <= o.N) && o.rows != WIDE;
-    if (!cols) store_block<TM, VECTOR, OT, ACT, ANYHOW, false, FNT>(acc, o.bias, p, false, mw, nw, lane);
-    else if (!rows) store_block<TM, VECTOR, OT, ACT, SOME_ROWS, false, FNT>(acc, o.bias, p, false, mw, nw, lane);
-    else if (p.R) store_block<TM, VECTOR, OT, ACT, WHOLE, true, FNT>(acc, o.bias, p, o.rows == EVEN, mw, nw, lane);
-    else store_block<TM, VECTOR, OT, ACT, WHOLE, false, FNT>(acc, o.bias, p, o.rows == EVEN, mw, nw, lane);
+    if (!cols) store_block<TM, VECTOR, OT, ACT, ANYHOW, false, FNT>(acc, o.bias, p, o.rows, mw, nw, lane);
+    else if (!rows) store_block<TM, VECTOR, OT, ACT, SOME_ROWS, false, FNT>(acc, o.bias, p, o.rows, mw, nw, lane);
+    else if (p.R) store_block<TM, VECTOR, OT, ACT, WHOLE, true, FNT>(acc, o.bias, p, o.rows, mw, nw, lane);
+    else store_block<TM, VECTOR, OT, ACT, WHOLE, false, FNT>(acc, o.bias, p, o.rows, mw, nw, lane);
 }
 
 }  // namespace sp24

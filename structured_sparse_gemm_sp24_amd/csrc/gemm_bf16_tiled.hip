@@ -272,7 +272,12 @@ hipError_t launch_gemm_bf16_tiled(const GemmArgs& g, hipStream_t s) {
     const double c128 = (double)(t128 / (2 * cus)) + (rem == 0 ? 0.0 : rem <= cus ? 0.6 : 1.0);
     const int64_t stages = (g.K + tiled_bf16::BK - 1) / tiled_bf16::BK;
     const bool wide = (stages >= 32 && 4 * t256 >= cus) || !(t256 < cus || (t256 <= 2 * cus && c128 <= c256));
-    if (g.epi.on) return g.tm ? launch_gemm_bf16_fused_tm(g, wide, s) : launch_gemm_bf16_fused_fm(g, wide, s);
+    if (g.epi.on && g.tm) return launch_gemm_bf16_fused_tm(g, wide, s);
+    // Feature-major with a fused epilogue (us, 128 wide / 256 wide, bias and GELU): the four waves of a 256-wide tile are alone on their
+    // SIMDs in the epilogue, while of two 128-wide workgroups one can multiply meanwhile: 512 x 128 over 32 x 784 26 / 34, 2048 x
+    // 2048 over 4 x 3136 (416 wide tiles) 93 / 107; a single turn of wide tiles over a long K 4096 x 4096 over 4096 90 / 85,
+    // 28672 x 8192 over 512 157 / 150.
+    if (g.epi.on) return launch_gemm_bf16_fused_fm(g, wide && stages >= 32 && t256 <= cus, s);
     if (wide) return g.tm ? launch_bn<true, 256, 1>(g, s) : launch_bn<false, 256, 1>(g, s);
     return g.tm ? launch_bn<true, 128, 2>(g, s) : launch_bn<false, 128, 2>(g, s);
 }
