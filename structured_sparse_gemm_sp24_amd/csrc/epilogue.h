@@ -216,33 +216,33 @@ __device__ __forceinline__ void finish1(int act, const Places& p, int type, floa
     }
 }
 
+template <int ACT>
+__device__ __forceinline__ f32x4 act4(f32x4 z) {
+    return f32x4{act_f32<ACT>(z[0]), act_f32<ACT>(z[1]), act_f32<ACT>(z[2]), act_f32<ACT>(z[3])};
+}
 __device__ __forceinline__ f32x4 act_any4(f32x4 z, int act) {
-    f32x4 y = z;
-#pragma unroll
-    for (int t = 0; t < 4; t++) y[t] = act_any(z[t], act);
-    return y;
+    if (act == ACT_NONE) return z;
+    return act == ACT_GELU ? act4<ACT_GELU>(z) : act == ACT_RELU ? act4<ACT_RELU>(z) : act4<ACT_SILU>(z);
 }
 
-// Four consecutive outputs of a row from column col on, `in` of them inside, the activation chosen at run time; what they
-// need is requested apart, to be on its way during the last sums.
+// Four consecutive outputs of a row from column col on, `in` of them inside, the activation chosen at run time, with bias and
+// residual that were requested before.
 template <int OT>
-struct Needed {
-    raw4<OT> r;
-    f32x4 b;
-};
-template <int OT>
-__device__ __forceinline__ Needed<OT> request4(const Epilogue& e, const Places& p, int64_t row, int64_t col, int in) {
-    Needed<OT> n = {};
-    if (p.R) n.r = read_in<OT>(p.R + (row * p.ldr + col) * (OT == T_FP32 ? 4 : 2), in);
-    if (e.bias) n.b = widen4<T_FP32>(read_in<T_FP32>(reinterpret_cast<const char*>(e.bias + col), in));
-    return n;
+__device__ __forceinline__ raw4<OT> residual4(const Places& p, int64_t row, int64_t col, int in) {
+    if (!p.R) return raw4<OT>{};
+    return read_in<OT>(p.R + (row * p.ldr + col) * (OT == T_FP32 ? 4 : 2), in);
+}
+__device__ __forceinline__ f32x4 bias4(const Epilogue& e, int64_t col, int in) {
+    if (!e.bias) return f32x4{0.f, 0.f, 0.f, 0.f};
+    return widen4<T_FP32>(read_in<T_FP32>(reinterpret_cast<const char*>(e.bias + col), in));
 }
 template <int OT>
-__device__ __forceinline__ void finish4(const Epilogue& e, const Places& p, const f32x4& acc, const Needed<OT>& n, int64_t row, int64_t col, int in) {
+__device__ __forceinline__ void finish4(const Epilogue& e, const Places& p, const f32x4& acc, const f32x4& b, const raw4<OT>& r, int64_t row,
+                                        int64_t col, int in) {
     constexpr int ES = OT == T_FP32 ? 4 : 2;
-    const f32x4 z = acc + n.b;
+    const f32x4 z = acc + b;
     f32x4 y = act_any4(z, e.act);
-    if (p.R) y += widen4<OT>(n.r);
+    if (p.R) y += widen4<OT>(r);
     if (p.Z) write_in<OT>(p.Z + (row * p.ldz + col) * ES, narrow4<OT>(z), in);
     write_in<OT>(p.Y + (row * p.ldy + col) * ES, narrow4<OT>(y), in);
 }
