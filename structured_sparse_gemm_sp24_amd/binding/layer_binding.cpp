@@ -202,6 +202,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         if (!any_grad) {
             grad = g.scalar_type();
             float_type(g, "a gradient");
+            TORCH_CHECK_TYPE(PyList_Check(S[i]) || PyTuple_Check(S[i]), "a state must be a list or tuple");
             bits8 = PySequence_Fast_GET_SIZE(S[i]) == 4;
         }
         any_grad = true;
