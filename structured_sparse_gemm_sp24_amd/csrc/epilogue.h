@@ -376,9 +376,8 @@ __device__ __forceinline__ void quad_transpose2(uint32_t (&a)[4], uint32_t (&b)[
 // Epilogue of a wave's 128 channels x 16 FNT tokens from accumulators acc(i, j) whose lane (q, r) holds channels 16 i + 4 q
 // .. +3 of token 16 j + r. The transposes of the plain product's stores run on the fp32 sums, so that activation and residual
 // work on the four consecutive outputs of a row that a lane stores: token-major four channels of a token, feature-major four
-// tokens of a channel. Groups of 16 rows x 64 columns, along a row first (token-major 256 consecutive bytes of a row go out
-// together: down the columns first 11008 x 4096 over 4096 tokens took 180 us without any epilogue, against 170). The residual of
-// a group is requested before the group in front of it is finished (HAS_R, 16-bit types, whole blocks; the other cases lack the
+// tokens of a channel. Groups of 16 rows x 64 columns, along a row first, so that token-major 256 consecutive bytes of a row go
+// out together. The residual of a group is requested before the group in front of it is finished (HAS_R, 16-bit types, whole blocks; the other cases lack the
 // registers, and whether there is a residual is then seen group by group). The bias is added as the sums lie; where they
 // are results of vector instructions (VECTOR), after the transposes, which takes fewer registers.
 template <bool TM, bool VECTOR, int OT, int ACT, int BLOCK, bool HAS_R, int FNT, typename Acc>

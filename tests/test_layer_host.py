@@ -50,7 +50,7 @@ BACK = dict(dY=A, dtype=BF16, N=100, M=33, lddy=33, Z=B, ldz=33, act=GELU, dZ=C,
 
 
 @pytest.mark.parametrize("bad,expect", [
-    (dict(dY=None), NULL), (dict(Z=None), NULL), (dict(dZ=None), NULL), (dict(workspace=None), NULL), (dict(dtype=I8), DTYPE), (dict(act=7), ARG),
+    (dict(dY=None), NULL), (dict(Z=None), NULL), (dict(dZ=None), NULL), (dict(N=1000, workspace=None), NULL), (dict(dtype=I8), DTYPE), (dict(act=7), ARG),
     (dict(act=0), ARG), (dict(act=0, Z=None), ARG), (dict(act=0, Z=None, dZ=None, dbias=None), NULL), (dict(N=0), SHAPE), (dict(M=0), SHAPE),
     (dict(N=1 << 31), SHAPE), (dict(M=(1 << 22) + 1, lddy=1 << 23, ldz=1 << 23, lddz=1 << 23), SHAPE), (dict(lddy=32), SHAPE), (dict(ldz=32), SHAPE),
     (dict(lddz=32), SHAPE), (dict(lddy=1 << 23), SHAPE), (dict(dY=MIS), ALIGN), (dict(Z=MIS), ALIGN), (dict(dZ=MIS), ALIGN),
