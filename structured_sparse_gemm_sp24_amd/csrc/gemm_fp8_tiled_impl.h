@@ -649,7 +649,10 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t s) {
     const int64_t T = (int64_t)a.tilesM * a.tilesN;
     // as many workgroups as fit walk the tiles; one tile each where a tile has a single stage (the pipeline across
     // tiles needs both buffers within one tile)
-    const int fit = (BN == 128 ? 2 : 1) * device_cus();
+    const int64_t cus = (BN == 128 ? 2 : 1) * device_cus();
+    // With an epilogue 64 tiles a workgroup at most, or two would share a bit of `apart`: a tile that is summed again without
+    // need may find its residual already overwritten by its output. (The plain product then only stores the same sums again.)
+    const int64_t fit = ACT == NO_EPILOGUE ? cus : cus * ((T + 64 * cus - 1) / (64 * cus));
     const dim3 grid((unsigned)(a.S >= NBUF && T > fit ? fit : T)), block(64 * Cfg<BN>::WAVES);
     if (g.out_fp16) hipLaunchKernelGGL((gemm_fp8_tiled_kernel<BN, true, ACT>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((gemm_fp8_tiled_kernel<BN, false, ACT>), grid, block, 0, s, a);

@@ -55,6 +55,26 @@ def test_fp8_output_past_the_caches(M, N, out):
     assert torch.equal(R, Y)
 
 
+def test_fp8_far_apart_scales_among_many_tiles():
+    """16576 tiles, more than 64 a workgroup, some of them summed again from memory; the residual's place is the output's."""
+    say("fp8 fused, far apart scales, 16576 tiles")
+    M, K, N = 28672, 144, 37888
+    W, X = sp.sp24_prune_mask(whole(1, M, K), 2)[1], whole(2, N, K)
+    far = [5, 20_000, 37_000, 37_800]
+    X[far, :128] *= 2.0 ** 70
+    X[far, 128:] *= 2.0 ** -30
+    w, (codes, scales) = sp.sp24_prune_compress_fp8(W), sp.sp24_quant_fp8(X)
+    R = torch.empty(N, M, dtype=BF16, device="cuda")
+    for i, part in enumerate(R.split(4096)):
+        part.copy_(rand(10 + i, *part.shape))
+    Y = sp.sp24_gemm_fp8_fused(*w, M, codes, scales, activation="relu", residual=R)
+    for i in (0, 18944, 36864):
+        near = torch.tensor([n not in far for n in range(i, i + 512)], device="cuda")
+        check(Y[i:i + 512][near], X[i:i + 512][near] @ W.t(), "relu", R[i:i + 512][near])
+    sp.sp24_gemm_fp8_fused(*w, M, codes, scales, activation="relu", residual=R, out=R)
+    assert torch.equal(R, Y)
+
+
 @pytest.mark.parametrize("which", ["Y", "Z", "R"])
 @pytest.mark.parametrize("layout,M,N", [("token", 260, 17), ("token", 256, 72), ("feature", 72, 136), ("feature", 40, 24)])
 def test_rows_of_128_megabytes(layout, M, N, which):
