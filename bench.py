@@ -88,8 +88,8 @@ class Kernel:
 def gemm_sources(N):
     """Sources of the bf16 GEMM kernels that can run at N tokens (the library picks among them by shape)."""
     if N >= TILED_MIN_N:
-        return ("gemm_bf16_tiled.hip", "sp24_device.h")
-    return ("gemm_bf16_fewtok.hip", "gemm_bf16_skinny.hip", "sp24_device.h")
+        return ("gemm_bf16_tiled.hip", "gemm_bf16_tiled_impl.h", "sp24_device.h")
+    return ("gemm_bf16_fewtok.hip", "gemm_bf16_skinny.hip", "gemm_bf16_skinny_impl.h", "sp24_device.h")
 
 
 # ----------------------------------------------------------------------------- oracle timing helpers

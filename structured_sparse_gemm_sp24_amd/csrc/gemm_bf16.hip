@@ -17,8 +17,8 @@
 // This file holds the direct kernel: each wave owns a 16-row x (16*NF)-column tile, takes A and the
 // index straight from global memory and gathers B element by element with bounds checks, through
 // general element strides, so it works for every shape, layout (feature- or token-major), batch and
-// row pitch. It serves the cases the others do not take: the few-token kernel (gemm_bf16_skinny.hip,
-// N <= 64) and the LDS-tiled kernel (gemm_bf16_tiled.hip, N > 64), each within its alignment and
+// row pitch. It serves the cases the others do not take: the few-token kernel (gemm_bf16_skinny_impl.h,
+// N <= 64) and the LDS-tiled kernel (gemm_bf16_tiled_impl.h, N > 64), each within its alignment and
 // size conditions.
 #include "epilogue.h"
 
