@@ -144,10 +144,13 @@ struct Outputs {
     int64_t ldy, ldz, ldr, sy, sz, sr, M, N;  // strides of batch entries in elements
     int64_t rows;  // one of these
 };
-// Rows of Y, Z and R: 16 of one take 2^31 bytes or more; every one on 8 (16-bit types) or 16 bytes, and then the whole of Y takes
-// 64 MB or more; else ODD. A residual is usually what was written last: a small one is read through the caches, which may
+// Rows of Y, Z and R: 16 of one take 2^31 bytes or more; every one on 8 (16-bit types) or 16 bytes, or on 64 where the outputs are large
+// (below), and then the whole of Y takes 64 MB or more; else ODD. A residual is usually what was written last: a small one is read through the caches, which may
 // still hold it (768 x 768 over 6304 tokens 16.4 us against 18.0, 512 x 128 over 32 x 784 23.8 against 31.3, buffers in turn), a large
 // one past them (11008 x 4096 over 4096 tokens 187 against 195).
+// Outputs go out past the caches. Where rows share 64-byte lines the caches join the pieces instead, once Y takes 8 MB with a Z beside it
+// or 32 MB alone (past the caches / through them: 11000 x 4096 over 4096 tokens with bias 202 / 187, with GELU and Z 266 / 217, 1000 x 768
+// over 20000 38.7 / 32.7, over 6304 with all 30.8 / 28.7; below 17.3 / 17.9, 512 x 128 over 32 x 784 with residual 24.4 / 25.8).
 enum { WIDE, ODD, EVEN, EVEN_LARGE };
 constexpr int OUTPUT_WORDS = sizeof(Outputs) / 4;
 static_assert(OUTPUT_WORDS <= 64, "a word a lane");
@@ -165,14 +168,15 @@ __device__ __forceinline__ Outputs kept_outputs(uint32_t kept) {
 }
 inline Outputs outputs_of(const Epilogue& e, void* Y, int64_t ldy, int64_t sy, int64_t M, int64_t N, int es, int64_t batch) {
     Outputs o{static_cast<char*>(Y), static_cast<char*>(e.Z), static_cast<const char*>(e.R), e.bias, ldy, e.ldz, e.ldr, sy, e.sz, e.sr, M, N, EVEN};
+    const int64_t bytes = M * N * batch * es, unit = bytes >= ((int64_t)(e.Z ? 8 : 32) << 20) ? 64 : 4 * es;
     const auto look = [&](const void* p, int64_t ld, int64_t stride) {
-        if (p && ((ld * es) % (4 * es) != 0 || (batch > 1 && (stride * es) % (4 * es) != 0)) && o.rows == EVEN) o.rows = ODD;
+        if (p && ((ld * es) % unit != 0 || (batch > 1 && (stride * es) % unit != 0)) && o.rows == EVEN) o.rows = ODD;
         if (p && ld * es * 16 >= ((int64_t)1 << 31)) o.rows = WIDE;
     };
     look(Y, ldy, sy);
     look(e.R, e.ldr, e.sr);
     look(e.Z, e.ldz, e.sz);
-    if (o.rows == EVEN && M * N * batch * es >= ((int64_t)64 << 20)) o.rows = EVEN_LARGE;
+    if (o.rows == EVEN && bytes >= ((int64_t)64 << 20)) o.rows = EVEN_LARGE;
     return o;
 }
 template <bool TM>
