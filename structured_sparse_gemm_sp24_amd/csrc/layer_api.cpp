@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t kMaxPitch = (int64_t)1 << 23, kMaxRows = ((int64_t)1 << 31) - 1, kMaxColumns = (int64_t)1 << 22;
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads in one launch
 constexpr int64_t kMaxElements = (int64_t)1 << 34;
+constexpr double kLeastEps = 0x1p-126;  // the least normal fp32: the step multiplies by 1 / (sqrt(v) + eps), which has to be finite
 
 bool aligned(const void* p, int to) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(to - 1)) == 0; }
 bool is_float(int dt) { return dt == SP24_BF16 || dt == SP24_FP16 || dt == SP24_FP32; }
@@ -100,7 +101,7 @@ int sp24_adamw(const sp24_adamw_tensor* tensors, int64_t count, int grad_dtype, 
     const bool later = lr_dev || step_dev, bits8 = state_dtype == SP24_FP8;
     if (later && !workspace) return SP24_ERR_NULL;
     if (!later && workspace) return SP24_ERR_ARG;
-    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(static_cast<float>(eps) > 0.f) || !finite_from_zero(eps)) return SP24_ERR_ARG;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= kLeastEps) || !finite_from_zero(eps)) return SP24_ERR_ARG;
     if ((!lr_dev && !finite_from_zero(lr)) || !finite_from_zero(weight_decay) || (!step_dev && step < 1)) return SP24_ERR_ARG;
     if (!aligned(lr_dev, 4) || !aligned(step_dev, 8) || !aligned(grad_scale, 4) || !aligned(workspace, 16)) return SP24_ERR_ALIGN;
     bool copies = false;

@@ -1,0 +1,34 @@
+"""The layer operators at the ends of what they accept."""
+import numpy as np
+import pytest
+import torch
+
+import structured_sparse_gemm_sp24_amd as sp
+from tests.gpu_util import require_gpu, say
+from tests.test_gpu_layer_adamw import HYPER, check, expect, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_least_eps(bits):
+    """With the least eps a weight without gradient stays zero, the others move by their formula."""
+    say(f"adamw least eps, {bits} bits")
+    hyper = {**HYPER, "eps": 2.0 ** -126}
+    p, g = rand(1, 3000), rand(2, 3000)
+    p[::3], g[::3] = 0, 0
+    state = sp.sp24_adamw_state(p, bits)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        for step in (1, 2, 3):
+            want = expect(p, g, state, step, seed=5, **hyper)
+            sp.sp24_adamw([p], [g], [state], step, seed=5, **hyper)
+            check(p, state, *want)
+            assert (p[::3] == 0).all() and torch.isfinite(p).all()
+    for eps in (1e-39, 0.0):
+        with pytest.raises(sp.Sp24Error):
+            sp.sp24_adamw([p], [g], [state], 4, **{**hyper, "eps": eps})
