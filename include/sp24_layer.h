@@ -91,7 +91,8 @@ typedef struct {
  *   captured graph then follows them); workspace: 16 bytes, 16-byte aligned, then required, else NULL.
  *   grad_scale: NULL, or a device fp32 (loss scaling, clipping by the global norm).
  *   0 <= beta < 1, eps from 2^-126 on (its reciprocal is an fp32 number), lr and weight_decay finite and >= 0, step >= 1. A v below 2^-126 may
- *   count as zero under the root, which then is off by less than 2^-63. n at most 2^34. One launch for every 32 tensors;
+ *   count as zero under the root, which then is off by less than 2^-63. 1 - lr weight_decay and lr / (1 - beta1^t) are held within
+ *   fp32's finite numbers. n at most 2^34. One launch for every 32 tensors;
  *   `tensors` is host memory, read before the call returns. Tensors must not overlap one another. */
 int sp24_adamw(const sp24_adamw_tensor* tensors, int64_t count, int grad_dtype, int state_dtype, int copy_dtype, double lr,
                const float* lr_dev, int64_t step, const int64_t* step_dev, double beta1, double beta2, double eps,

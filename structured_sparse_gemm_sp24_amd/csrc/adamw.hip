@@ -22,10 +22,16 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     return x ^ (x >> 16);
 }
 
+// x as fp32, at most the largest finite one: an infinite rate would make NaN of a weight that has nothing to change.
+__host__ __device__ inline float finite(double x) {
+    constexpr double MOST = 3.4028234663852886e+38;
+    return (float)(x > MOST ? MOST : x < -MOST ? -MOST : x);
+}
+
 __host__ __device__ inline AdamScalars scalars_of(const AdamSchedule& h, double lr, int64_t step) {
     AdamScalars a;
-    a.decay = (float)(1.0 - lr * h.decay);
-    a.rate = (float)(lr / (1.0 - pow(h.beta1, (double)step)));
+    a.decay = finite(1.0 - lr * h.decay);
+    a.rate = finite(lr / (1.0 - pow(h.beta1, (double)step)));
     a.root = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)step)));
     a.key = mix(mix(mix((uint32_t)h.seed) ^ (uint32_t)(h.seed >> 32)) ^ (uint32_t)step);
     return a;

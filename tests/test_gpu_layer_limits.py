@@ -32,3 +32,17 @@ def test_adamw_least_eps(bits):
     for eps in (1e-39, 0.0):
         with pytest.raises(sp.Sp24Error):
             sp.sp24_adamw([p], [g], [state], 4, **{**hyper, "eps": eps})
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("later", [False, True])
+@pytest.mark.parametrize("lr,decay", [(3.4e38, 0.0), (1e10, 3e38), (3e38, 3e38)])
+def test_adamw_rates_past_fp32(bits, later, lr, decay):
+    """Where lr / (1 - beta1^t) or lr weight_decay pass fp32 a weight that has nothing to change stays zero."""
+    say(f"adamw rates past fp32, {bits} bits, lr {lr}, decay {decay}, on the device {later}")
+    p, g = torch.zeros(1000, device="cuda"), torch.zeros(1000, device="cuda")
+    p[500:], g[500:] = 1.0, 1.0
+    state = sp.sp24_adamw_state(p, bits)
+    rate = torch.tensor(lr, device="cuda") if later else lr
+    sp.sp24_adamw([p], [g], [state], 1, lr=rate, weight_decay=decay)
+    assert (p[:500] == 0).all() and not (p[500:] == 1).any()
