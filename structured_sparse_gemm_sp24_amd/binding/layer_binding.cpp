@@ -175,12 +175,14 @@ const Tensor* device_scalar(PyObject* o, const char* name, const Tensor& first, 
     return &t;
 }
 
-// adamw(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed, copies, params_out, states_out)
+// adamw(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed, copies, params_out, states_out, first_index)
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
-    SP24_ARGS(14);
+    SP24_ARGS(15);
     TORCH_CHECK_TYPE(PyList_Check(a[0]) || PyTuple_Check(a[0]), "params must be a list or tuple");
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(a[0]);
+    const int64_t first_index = integer(a[14], "first_index");
+    TORCH_CHECK_VALUE(first_index >= 0 && first_index <= (int64_t{1} << 32) - n, "first_index must be a place in the model below 2^32, not ", first_index);
     if (n == 0) Py_RETURN_NONE;
     PyObject** const P = PySequence_Fast_ITEMS(a[0]);
     PyObject** const G = items(a[1], "grads", n);
@@ -209,7 +211,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
         const auto shape = p.sizes();
         sp24_adamw_tensor t = {};
         t.n = p.numel();
-        t.index = i;
+        t.index = first_index + i;
         t.p = static_cast<const float*>(flat(P[i], "a parameter", first, at::kFloat, shape));
         t.p_out = static_cast<float*>(flat(PO[i], "a parameter of out", first, at::kFloat, shape));
         t.g = flat(G[i], "a gradient", first, grad, shape);

@@ -90,12 +90,13 @@ def sp24_adamw_state(param: torch.Tensor, bits: int = 32) -> tuple:
 
 
 def sp24_adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
-               grad_scale: torch.Tensor | None = None, seed: int = 0, copies=None, out=None) -> None:
+               grad_scale: torch.Tensor | None = None, seed: int = 0, copies=None, out=None, first_index: int = 0) -> None:
     """One step of AdamW over a list of fp32 parameters (contiguous, on one device), in place: grads of one 16- or 32-bit type
     (None passes a parameter over), states from sp24_adamw_state, of one kind. ``step`` counts from 1; it and ``lr`` may be
     device tensors (int64 and fp32) that are read when the kernels run, as a captured graph needs. ``grad_scale`` (a device fp32)
     multiplies the gradients. ``copies``: bf16 or fp16 tensors (or None) that receive the new weights rounded. ``seed``: of the
-    random rounding of 8-bit states. ``out``: (parameters, states) to write to instead."""
+    random rounding of 8-bit states, which also takes the parameter's place in the model: ``first_index`` is that of params[0], so
+    that groups of parameters with a call each round independently. ``out``: (parameters, states) to write to instead."""
     params_out, states_out = (None, None) if out is None else out
     (_native or _load_native()).adamw(params, grads, states, step, lr, betas[0], betas[1], eps, weight_decay, grad_scale, seed, copies,
-                                      params_out, states_out)
+                                      params_out, states_out, first_index)

@@ -46,3 +46,25 @@ def test_adamw_rates_past_fp32(bits, later, lr, decay):
     rate = torch.tensor(lr, device="cuda") if later else lr
     sp.sp24_adamw([p], [g], [state], 1, lr=rate, weight_decay=decay)
     assert (p[:500] == 0).all() and not (p[500:] == 1).any()
+
+
+def test_adamw_groups_round_independently():
+    """Two calls, each with its parameters' places in the model, are one call over all of them; without, equal parameters would
+    share their random bits from call to call."""
+    say("adamw groups")
+    g = [rand(1, 5000)] * 4 + [rand(2, 300)]
+    p = [torch.zeros_like(x) for x in g]
+    one, two = ([sp.sp24_adamw_state(x, 8) for x in p] for _ in range(2))
+    sp.sp24_adamw(p, g, one, 1, seed=3, first_index=7)
+    at = 2
+    sp.sp24_adamw(p[:at], g[:at], two[:at], 1, seed=3, first_index=7)
+    sp.sp24_adamw(p[at:], g[at:], two[at:], 1, seed=3, first_index=7 + at)
+    for a, b in zip(one, two):
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+    for i in range(4):
+        for j in range(i):
+            assert not torch.equal(one[i][0].view(torch.uint8), one[j][0].view(torch.uint8))
+    want = expect(torch.zeros(300, device="cuda"), g[4], sp.sp24_adamw_state(p[4], 8), 1, index=11, seed=3, lr=1e-3, weight_decay=0.01)
+    check(p[4], two[4], want[0], np.full(300, np.inf), want[2])  # the state; two calls moved the weight
+    last = [torch.zeros(8, device="cuda")]
+    sp.sp24_adamw(last, last, [sp.sp24_adamw_state(last[0], 8)], 1, first_index=2 ** 32 - 1)

@@ -1,5 +1,6 @@
 """Limits of the layer operators' arguments, checked on the host before any HIP call (no GPU, no kernel launched)."""
 import pytest
+import torch
 
 import structured_sparse_gemm_sp24_amd as sp
 from tests.test_abi import lib  # noqa: F401
@@ -20,3 +21,14 @@ def test_eps_with_an_infinite_reciprocal_is_refused(lib, state, eps):  # noqa: F
 def test_least_eps_is_taken(lib):  # noqa: F811
     """No tensors, so that nothing is launched where there is a device."""
     assert lib.sp24_adamw(None, *changed(ADAM, count=0, eps=2.0 ** -126)) in (sp.SP24_OK, sp.SP24_ERR_DEVICE)
+
+
+def test_places_in_the_model_are_below_2_to_32():
+    p = [torch.zeros(8)] * 2
+    for first in (-1, 2 ** 32 - 1, 2 ** 63 - 1):
+        with pytest.raises(ValueError, match="first_index"):
+            sp.sp24_adamw(p, p, [sp.sp24_adamw_state(x) for x in p], 1, first_index=first)
+    with pytest.raises(TypeError):
+        sp.sp24_adamw(p, p, [sp.sp24_adamw_state(x) for x in p], 1, first_index=0.5)
+    with pytest.raises(ValueError, match="device"):  # a good one: the next check, that of the tensors
+        sp.sp24_adamw(p, p, [sp.sp24_adamw_state(x) for x in p], 1, first_index=2 ** 32 - 2)
