@@ -4,7 +4,8 @@
 
 #include <torch/csrc/utils/tensor_dtypes.h>
 
-#include <unordered_set>
+#include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "../../include/sp24_layer.h"
@@ -175,6 +176,11 @@ const Tensor* device_scalar(PyObject* o, const char* name, const Tensor& first, 
     return &t;
 }
 
+// What a step writes of a tensor, each with the input that it may be.
+std::array<std::pair<const void*, const void*>, 6> written_by(const sp24_adamw_tensor& t) {
+    return {{{t.p_out, t.p}, {t.m_out, t.m}, {t.v_out, t.v}, {t.m_scales_out, t.m_scales}, {t.v_scales_out, t.v_scales}, {t.copy, nullptr}}};
+}
+
 // adamw(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed, copies, params_out, states_out, first_index)
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
@@ -197,7 +203,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     bool any_grad = false, any_copy = false, bits8 = false;
     std::vector<sp24_adamw_tensor> list;
     list.reserve(n);
-    std::unordered_set<void*> seen;
+    std::unordered_map<const void*, const void*> written;  // what the step writes, and the input beside it
     for (Py_ssize_t i = 0; i < n; i++) {
         if (is_none(G[i])) continue;  // no gradient: the tensor stays as it is
         const Tensor &p = tensor(P[i], "a parameter"), &g = tensor(G[i], "a gradient");
@@ -243,11 +249,16 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             t.copy = flat(C[i], "a copy", first, copy, shape);
         }
         if (t.n)
-            for (void* written : {static_cast<void*>(t.p_out), t.m_out, t.v_out, static_cast<void*>(t.copy)})
-                TORCH_CHECK_VALUE(written == nullptr || seen.insert(written).second, "a tensor is given twice");
+            for (const auto& [to, from] : written_by(t)) TORCH_CHECK_VALUE(to == nullptr || written.emplace(to, from).second, "a tensor is given twice");
         list.push_back(t);
     }
     if (!any_grad) Py_RETURN_NONE;
+    if (PO != P || SO != S)  // in place every input is what is written in its place
+        for (const auto& t : list)
+            for (const auto& [to, from] : written_by(t)) {
+                const auto at = from && t.n ? written.find(from) : written.end();
+                TORCH_CHECK_VALUE(at == written.end() || at->second == from, "a tensor of out is the input of another");
+            }
     const Tensor* const step_dev = device_scalar(a[3], "step", first, at::kLong);
     const Tensor* const lr_dev = device_scalar(a[4], "lr", first, at::kFloat);
     const Tensor* const scale = device_scalar(a[9], "grad_scale", first, at::kFloat);

@@ -68,3 +68,26 @@ def test_adamw_groups_round_independently():
     check(p[4], two[4], want[0], np.full(300, np.inf), want[2])  # the state; two calls moved the weight
     last = [torch.zeros(8, device="cuda")]
     sp.sp24_adamw(last, last, [sp.sp24_adamw_state(last[0], 8)], 1, first_index=2 ** 32 - 1)
+
+
+def test_adamw_refuses_tensors_in_two_roles():
+    """Scales that two moments share, and outputs that another tensor still reads: which comes first would be left to chance."""
+    say("adamw refuses tensors in two roles")
+    p, g = [rand(i, 256) for i in range(2)], [rand(9, 256)] * 2
+    for bits in (32, 8):
+        s = [sp.sp24_adamw_state(x, bits) for x in p]
+        t = [sp.sp24_adamw_state(x, bits) for x in p]
+        q = [torch.empty_like(x) for x in p]
+        for out in ((p[::-1], s), (p, s[::-1]), ([p[1], q[0]], t), (q, [s[1], t[0]]), (q, [(t[0][0], *s[1][1:]), t[1]])):
+            with pytest.raises(ValueError):
+                sp.sp24_adamw(p, g, s, 1, out=out)
+        if bits == 8:
+            with pytest.raises(ValueError):
+                sp.sp24_adamw(p, g, [(s[0][0], s[0][1], s[0][2], s[0][1]), s[1]], 1)
+            with pytest.raises(ValueError):
+                sp.sp24_adamw(p, g, [s[0], (s[1][0], s[0][1], s[1][2], s[1][3])], 1)
+        before = [x.clone() for x in p]
+        sp.sp24_adamw(p, g, s, 1, out=(q, t))  # elsewhere, in place, and some of each
+        sp.sp24_adamw(p, g, s, 1, out=([p[0], q[1]], [t[0], s[1]]))
+        assert torch.equal(p[0], q[0]) and torch.equal(p[1], before[1]) and not torch.equal(q[1], p[1])
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(s[1], t[1]))
