@@ -55,7 +55,7 @@ def sp24_gemm_bf16_fused(values: torch.Tensor, meta: torch.Tensor, M: int, X: to
     """Y = act(W X + bias) + residual for a 2:4 weight in bf16, layouts and batches as sp24_gemm_bf16_ex. activation: "none",
     "gelu", "relu" or "silu"; bias fp32[M]; residual of Y's type and shape (give it as ``out`` too to add in place; a batch
     may share one through a stride of 0). With ``preact`` (True, or a tensor to fill) returns (Y, Z), Z = W X + bias
-    rounded to Y's type: what sp24_epilogue_backward needs."""
+    rounded to Y's type: what sp24_epilogue_backward needs. A batch's entries lie on 16 bytes: where their size is no multiple of that, give ``out`` (and ``preact``) with strides that are."""
     return (_native or _load_native()).gemm_bf16(values, meta, M, X, bias, _activation(activation), residual, preact, _layout(layout), out_dtype, out)
 
 

@@ -91,3 +91,39 @@ def test_adamw_refuses_tensors_in_two_roles():
         sp.sp24_adamw(p, g, s, 1, out=([p[0], q[1]], [t[0], s[1]]))
         assert torch.equal(p[0], q[0]) and torch.equal(p[1], before[1]) and not torch.equal(q[1], p[1])
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(s[1], t[1]))
+
+
+def strided(batch, rows, cols, dtype, fill=float("nan")):
+    """(buffer, its entries of rows x cols whose strides are the least multiples of 16 bytes, plus 16)."""
+    unit = 16 // dtype.itemsize
+    entry = (-(-rows * cols // unit) + 1) * unit
+    buf = torch.full((batch, entry), fill, dtype=dtype, device="cuda")
+    return buf, buf.as_strided((batch, rows, cols), (entry, cols, 1))
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout,M,K,N", [("token", 70, 64, 30), ("token", 7, 128, 1), ("token", 33, 64, 131), ("feature", 30, 64, 70), ("feature", 257, 128, 129), ("feature", 9, 48, 5)])
+def test_batched_entries_of_odd_sizes(layout, M, K, N, out):
+    """Entries that are no multiple of 16 bytes, in outputs and residuals of padded strides: each as by itself, nothing beside it written."""
+    say(f"bf16 fused batch of odd entries {layout} {M}x{K} N={N} {out}")
+    values, meta = sp.sp24_prune_compress(rand(1, M, K, dtype=torch.bfloat16))
+    X = rand(2, 3, *((N, K) if layout == "token" else (K, N)), dtype=torch.bfloat16)
+    if layout == "feature":  # X's entries lie on 16 bytes too
+        x = strided(3, K, N, torch.bfloat16)[1]
+        X = x.copy_(X)
+    bias, shape = rand(3, M), ((N, M) if layout == "token" else (M, N))
+    ybuf, Y = strided(3, *shape, out)
+    zbuf, Z = strided(3, *shape, out)
+    _, R = strided(3, *shape, out)
+    R.copy_(rand(4, 3, *shape))
+    how = dict(bias=bias, activation="silu", layout=layout, out_dtype=out)
+    got = sp.sp24_gemm_bf16_fused(values, meta, M, X, residual=R, preact=Z, out=Y, **how)
+    assert got[0].data_ptr() == Y.data_ptr() and got[1].data_ptr() == Z.data_ptr()
+    for b in range(3):
+        one = sp.sp24_gemm_bf16_fused(values, meta, M, X[b].contiguous(), residual=R[b].contiguous(), preact=True, **how)
+        assert torch.equal(Y[b], one[0]) and torch.equal(Z[b], one[1])
+    for buf in (ybuf, zbuf):
+        assert torch.isnan(buf[:, shape[0] * shape[1]:]).all()
+    inplace = strided(3, *shape, out)[1].copy_(R)
+    sp.sp24_gemm_bf16_fused(values, meta, M, X, residual=inplace, out=inplace, **how)
+    assert torch.equal(inplace, Y)
