@@ -14,7 +14,7 @@
  *   GELU(z) = z Phi(z) as in sp24_gemm_i8_fused, |error| <= 8 * 2^-24 |z|; SiLU(z) = z / (1 + e^-z), within
  *   (6 + 3 |z|) * 2^-24 of itself (z >= -87); ReLU(z) = max(z, 0). Infinities have their limits, NaN stays NaN.
  * R and Z have a base aligned to 16 bytes and any pitch of at least a row. R may be Y (same base, pitch and batch
- * stride: each element is read before it is written); Z must overlap neither.
+ * stride: each element is read before it is written) and shares no element with it otherwise; Z shares none with either.
  */
 #ifndef SP24_LAYER_H
 #define SP24_LAYER_H
@@ -44,6 +44,8 @@ int sp24_gemm_fp8_fused(const uint8_t* values, const uint8_t* meta, const uint8_
  *   dZ[n, m] = dY[n, m] act'(Z[n, m]),  dbias[m] = sum_n dY[n, m] act'(Z[n, m])  (fp32[M], from unrounded products).
  * dZ is what sp24_grad_weight_fp8 and the input's gradient take; the residual's gradient is dY itself. ReLU' is 1 where
  * Z > 0 and chooses: dZ is +0 elsewhere whatever dY holds.
+ * Of a feature-major product's Z (M x N, an entry a call) this gives dZ alone: rows are then channels, dbias would be a sum
+ * over channels and is left NULL, and the bias's gradient, one along rows, is not offered.
  *   dY, Z, dZ: N x M of dtype (BF16, FP16 or FP32), base 16-byte aligned, any pitch of at least M and below 2^23. dZ may be
  *   dY or Z (same base and pitch). dbias: NULL where there is no bias. With SP24_ACT_NONE dZ would be dY: Z and dZ must
  *   be NULL and dbias not. N below 2^31, M at most 2^22. workspace: sp24_epilogue_backward_bytes(N, M) bytes (may be

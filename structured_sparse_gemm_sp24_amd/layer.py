@@ -55,7 +55,8 @@ def sp24_gemm_bf16_fused(values: torch.Tensor, meta: torch.Tensor, M: int, X: to
     """Y = act(W X + bias) + residual for a 2:4 weight in bf16, layouts and batches as sp24_gemm_bf16_ex. activation: "none",
     "gelu", "relu" or "silu"; bias fp32[M]; residual of Y's type and shape (give it as ``out`` too to add in place; a batch
     may share one through a stride of 0). With ``preact`` (True, or a tensor to fill) returns (Y, Z), Z = W X + bias
-    rounded to Y's type: what sp24_epilogue_backward needs. A batch's entries lie on 16 bytes: where their size is no multiple of that, give ``out`` (and ``preact``) with strides that are."""
+    rounded to Y's type: what sp24_epilogue_backward needs, token-major (feature-major it gives dZ alone). A batch's entries
+    lie on 16 bytes: where their size is no multiple of that, give ``out`` (and ``preact``) with strides that are."""
     return (_native or _load_native()).gemm_bf16(values, meta, M, X, bias, _activation(activation), residual, preact, _layout(layout), out_dtype, out)
 
 
@@ -72,7 +73,8 @@ def sp24_epilogue_backward(dY: torch.Tensor, preact: torch.Tensor | None = None,
                            dbias: torch.Tensor | None = None, want_dbias: bool = True):
     """Gradients of the products' epilogue (token-major): (dZ, dbias) with dZ = dY act'(preact) of dY's type, what the weight's
     and the input's gradients take, and dbias its sum over tokens (fp32[M]; None with want_dbias=False and no ``dbias``).
-    ``dZ`` may be dY or preact. Without an activation dZ is dY itself. The residual's gradient is dY."""
+    ``dZ`` may be dY or preact. Without an activation dZ is dY itself. The residual's gradient is dY. Of feature-major
+    matrices, an entry of a batch a call, take dZ with want_dbias=False: the sum that dbias holds would be one over channels."""
     return (_native or _load_native()).epilogue_backward(dY, preact, _activation(activation), dZ, dbias, bool(want_dbias))
 
 

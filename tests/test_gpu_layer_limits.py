@@ -127,3 +127,14 @@ def test_batched_entries_of_odd_sizes(layout, M, K, N, out):
     inplace = strided(3, *shape, out)[1].copy_(R)
     sp.sp24_gemm_bf16_fused(values, meta, M, X, residual=inplace, out=inplace, **how)
     assert torch.equal(inplace, Y)
+
+
+@pytest.mark.parametrize("act", ["gelu", "relu", "silu"])
+def test_feature_major_gradient_without_bias(act):
+    """dZ of a feature-major Z is the token-major one's transpose."""
+    say(f"feature-major epilogue gradient {act}")
+    for dtype in (torch.bfloat16, torch.float32):
+        dY, Z = rand(1, 130, 196, dtype=dtype), rand(2, 130, 196, dtype=dtype)
+        dZ, none = sp.sp24_epilogue_backward(dY, Z, act, want_dbias=False)
+        want, _ = sp.sp24_epilogue_backward(dY.t().contiguous(), Z.t().contiguous(), act)
+        assert none is None and torch.equal(dZ, want.t())
