@@ -88,8 +88,8 @@ class Kernel:
 def gemm_sources(N):
     """Sources of the bf16 GEMM kernels that can run at N tokens (the library picks among them by shape)."""
     if N >= TILED_MIN_N:
-        return ("gemm_bf16_tiled.hip", "gemm_bf16_tiled_impl.h", "sp24_device.h")
-    return ("gemm_bf16_fewtok.hip", "gemm_bf16_skinny.hip", "gemm_bf16_skinny_impl.h", "sp24_device.h")
+        return ("gemm_bf16_tiled.hip", "gemm_bf16_tiled_impl.h", "epilogue.h", "fp8_device.h", "sp24_device.h")
+    return ("gemm_bf16_fewtok.hip", "gemm_bf16_skinny.hip", "gemm_bf16_skinny_impl.h", "epilogue.h", "fp8_device.h", "sp24_device.h")
 
 
 # ----------------------------------------------------------------------------- oracle timing helpers
@@ -189,7 +189,7 @@ def _bf16_gemm_workload(name, W_host, X_host, score, Xcal_host, config, layout, 
         "prune_compress",
         lambda c: sp.sp24_prune_compress(c["W"], score=score, norms=c["norms"] if wanda else None, values=c["vals"],
                                          meta=c["meta"]),
-        M * K * 2 + (K * 4 if wanda else 0) + M * K * 9 // 8, sources=("prune.hip", "sp24_device.h")))
+        M * K * 2 + (K * 4 if wanda else 0) + M * K * 9 // 8, sources=("prune.hip", "fp8_device.h", "sp24_device.h")))
     lay = "token" if tm else "feature"
     kernels.append(Kernel("gemm_bf16",
                           lambda c: sp.sp24_gemm_bf16_ex(c["vals"], c["meta"], M, c["X"], layout=lay, out=c["Y"]),
@@ -306,7 +306,7 @@ def workload_single(args):
     kernels = [
         Kernel("prune_compress", lambda c: sp.sp24_prune_compress(c["W"], val_dtype=torch.bfloat16, values=c["vals"],
                                                                   meta=c["meta"]),
-               M * K * 4 + M * K * 9 // 8, sources=("prune.hip", "sp24_device.h")),
+               M * K * 4 + M * K * 9 // 8, sources=("prune.hip", "fp8_device.h", "sp24_device.h")),
         Kernel("gemm_bf16", lambda c: sp.sp24_gemm_bf16_ex(c["vals"], c["meta"], M, c["X"], layout=args.layout,
                                                            out=c["Y"]),
                M * K * 9 // 8 + K * N * 2 + M * N * 4, float(M) * N * K, "bf16", gemm_sources(N))]
@@ -365,7 +365,7 @@ def workload_bert_int8(args):
         M, K, N = L["M"], L["K"], L["N"]
         kernels.append(Kernel(f"prune_compress_i8_w{i + 1}",
                               lambda c, i=i: sp.sp24_prune_compress(c[i]["W"], values=c[i]["vals"], meta=c[i]["meta"]),
-                              M * K + M * K * 5 // 8, sources=("prune.hip", "sp24_device.h")))
+                              M * K + M * K * 5 // 8, sources=("prune.hip", "fp8_device.h", "sp24_device.h")))
         kernels.append(Kernel(f"gemm_i8_w{i + 1}",
                               lambda c, i=i, M=M: sp.sp24_gemm_i8_ex(c[i]["vals"], c[i]["meta"], M, c[i]["X"],
                                                                      scale=c[i]["scale"], layout=args.layout,
@@ -451,9 +451,9 @@ def workload_bert_int8_fused(args):
     srcs = ("gemm_i8_tiled_impl.h", "gemm_i8_tiled_i8.hip", "sp24_device.h")
     kernels = [
         Kernel("prune_compress_i8_w1", lambda c: sp.sp24_prune_compress(c["W1"], values=c["v0"], meta=c["m0"]),
-               M1 * K1 + M1 * K1 * 5 // 8, sources=("prune.hip", "sp24_device.h")),
+               M1 * K1 + M1 * K1 * 5 // 8, sources=("prune.hip", "fp8_device.h", "sp24_device.h")),
         Kernel("prune_compress_i8_w2", lambda c: sp.sp24_prune_compress(c["W2"], values=c["v1"], meta=c["m1"]),
-               M2 * K2 + M2 * K2 * 5 // 8, sources=("prune.hip", "sp24_device.h")),
+               M2 * K2 + M2 * K2 * 5 // 8, sources=("prune.hip", "fp8_device.h", "sp24_device.h")),
         Kernel("gemm_i8_w1_gelu_i8out",
                lambda c: sp.sp24_gemm_i8_fused(c["v0"], c["m0"], M1, c["X"], c["s1"], bias=c["b1"], activation="gelu",
                                                out_dtype=torch.int8, out_scale=s_h, layout=lay, out=c["H"]),
@@ -522,7 +522,7 @@ def workload_llm_int8(args):
                            meta=torch.empty(mb, dtype=torch.uint8, device="cuda"),
                            Y=torch.empty((N, M), dtype=torch.float32, device="cuda")))
     kernels = [Kernel("prune_compress_i8", lambda c: sp.sp24_prune_compress(c["W"], values=c["vals"], meta=c["meta"]),
-                      M * K + M * K * 5 // 8, sources=("prune.hip", "sp24_device.h")),
+                      M * K + M * K * 5 // 8, sources=("prune.hip", "fp8_device.h", "sp24_device.h")),
                Kernel("gemm_i8", lambda c: sp.sp24_gemm_i8_ex(c["vals"], c["meta"], M, c["X"], scale=c["scale"],
                                                               layout="token", out=c["Y"]),
                       kernel_bytes, float(M) * N * K, "i8", ("gemm_i8_fewtok.hip", "sp24_device.h"))]
