@@ -122,8 +122,9 @@ __global__ __launch_bounds__(256) void add_parts_kernel(const float* parts, int 
 }
 
 // Threads along a row: pieces of 128 bytes (16-bit types) of many rows, or of a KB. The short ones give more workgroups where rows
-// are few or short (2048 x 4096 bf16 GELU 19.8 us against 21.2, 6304 x 768 18.4 / 20.2), the long ones read long rows faster (8192 x
-// 28672 289 / 325, rows at any element 4096 x 11007 96 / 135), both with at least 16 rows a thread.
+// are few or short (short / long, bf16 GELU: 2048 x 4096 15.1 us / 19.9, 6304 x 768 13.0 / 26.8, 513 x 8192 10.4 / 12.0, 400 x 28672 18.8 /
+// 20.8), the long ones read long rows faster (8192 x 28672 325 / 288, rows at any element 4096 x 11007 120 / 93, 4096 x 8192 46.9 /
+// 44.0; many rows of 5000 to 8191, which the rule leaves to the short ones, too: 4096 x 7168 44 / 40, SiLU 8192 x 5120 63 / 56).
 constexpr int LONG = 64, SHORT = 8;
 
 int threads_along(int64_t N, int64_t M) { return M < 8192 || N <= 512 ? SHORT : LONG; }
