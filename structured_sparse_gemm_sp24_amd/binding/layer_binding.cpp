@@ -4,7 +4,6 @@
 
 #include <torch/csrc/utils/tensor_dtypes.h>
 
-#include <unordered_map>
 #include <utility>
 #include <vector>
 
@@ -181,6 +180,25 @@ std::array<std::pair<const void*, const void*>, 6> written_by(const sp24_adamw_t
     return {{{t.p_out, t.p}, {t.m_out, t.m}, {t.v_out, t.v}, {t.m_scales_out, t.m_scales}, {t.v_scales_out, t.v_scales}, {t.copy, nullptr}}};
 }
 
+// The written addresses of a step and their inputs, in a flat table: with a node for each a call of 100 tensors takes 30 us (8 bits 48), so
+// 20 (23).
+class Written {
+    std::vector<std::pair<const void*, const void*>> slots;
+    int shift;
+
+public:
+    explicit Written(size_t most) : shift(63) {
+        while ((size_t{1} << (64 - shift)) < 2 * most) shift--;
+        slots.resize(size_t{1} << (64 - shift));
+    }
+    // The slot of an address, or the free one that it would take.
+    std::pair<const void*, const void*>& at(const void* x) {
+        size_t i = static_cast<size_t>(reinterpret_cast<uintptr_t>(x) * 0x9E3779B97F4A7C15ull >> shift);
+        while (slots[i].first != nullptr && slots[i].first != x) i = (i + 1) & (slots.size() - 1);
+        return slots[i];
+    }
+};
+
 // adamw(params, grads, states, step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed, copies, params_out, states_out, first_index)
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
@@ -203,7 +221,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     bool any_grad = false, any_copy = false, bits8 = false;
     std::vector<sp24_adamw_tensor> list;
     list.reserve(n);
-    std::unordered_map<const void*, const void*> written;  // what the step writes, and the input beside it
+    Written written(6 * n);
     for (Py_ssize_t i = 0; i < n; i++) {
         if (is_none(G[i])) continue;  // no gradient: the tensor stays as it is
         const Tensor &p = tensor(P[i], "a parameter"), &g = tensor(G[i], "a gradient");
@@ -249,15 +267,21 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
             t.copy = flat(C[i], "a copy", first, copy, shape);
         }
         if (t.n)
-            for (const auto& [to, from] : written_by(t)) TORCH_CHECK_VALUE(to == nullptr || written.emplace(to, from).second, "a tensor is given twice");
+            for (const auto& [to, from] : written_by(t)) {
+                if (to == nullptr) continue;
+                auto& slot = written.at(to);
+                TORCH_CHECK_VALUE(slot.first == nullptr, "a tensor is given twice");
+                slot = {to, from};
+            }
         list.push_back(t);
     }
     if (!any_grad) Py_RETURN_NONE;
     if (PO != P || SO != S)  // in place every input is what is written in its place
         for (const auto& t : list)
             for (const auto& [to, from] : written_by(t)) {
-                const auto at = from && t.n ? written.find(from) : written.end();
-                TORCH_CHECK_VALUE(at == written.end() || at->second == from, "a tensor of out is the input of another");
+                if (from == nullptr || t.n == 0) continue;
+                const auto& slot = written.at(from);
+                TORCH_CHECK_VALUE(slot.first == nullptr || slot.second == from, "a tensor of out is the input of another");
             }
     const Tensor* const step_dev = device_scalar(a[3], "step", first, at::kLong);
     const Tensor* const lr_dev = device_scalar(a[4], "lr", first, at::kFloat);
