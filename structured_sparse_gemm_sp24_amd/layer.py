@@ -94,7 +94,7 @@ def sp24_adamw_state(param: torch.Tensor, bits: int = 32) -> tuple:
 def sp24_adamw(params, grads, states, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                grad_scale: torch.Tensor | None = None, seed: int = 0, copies=None, out=None, first_index: int = 0) -> None:
     """One step of AdamW over a list of fp32 parameters (contiguous, on one device), in place: grads of one 16- or 32-bit type
-    (None passes a parameter over), states from sp24_adamw_state, of one kind. ``step`` counts from 1; it and ``lr`` may be
+    (None passes a parameter over, and its places in ``copies`` and ``out``), states from sp24_adamw_state, of one kind. ``step`` counts from 1; it and ``lr`` may be
     device tensors (int64 and fp32) that are read when the kernels run, as a captured graph needs. ``grad_scale`` (a device fp32)
     multiplies the gradients. ``copies``: bf16 or fp16 tensors (or None) that receive the new weights rounded. ``seed``: of the
     random rounding of 8-bit states, which also takes the parameter's place in the model: ``first_index`` is that of params[0], so
